@@ -315,6 +315,127 @@ GLA_API gla_status gla_mlstm_bwd_saved(const gla_problem* p, const void* q, cons
                                        void* dq, void* dk, void* dv, float* dg, float* ditil, void* ws,
                                        size_t ws_bytes, void* stream);
 
+/* Gated linear recurrence with a vector state: every channel d of a head is a recurrence of its
+ * own (the diagonal member of the family above: the state is a vector, not a matrix),
+ *     h_t = alpha_t * h_{t-1} + m(alpha_t) * x_t,   o_t = h_t,   alpha_t = exp(g_t),
+ * elementwise, from h_{-1} = h0 (or 0), with h_{L-1} = hT. `input` is a gla_scan_input and picks
+ * the factor m on the input: 1; 1 - alpha (a convex mix of state and input); or
+ * sqrt(1 - alpha^2) (the state keeps the input's variance).
+ * p: B, H, L >= 0; Dk = Dv = D, the channels per head, 1 <= D <= 65536; io; gate must be
+ *   GLA_GATE_PER_KEY; chunk, scale and plan are ignored.
+ * x, o, dO, dx [B,H,L,D] in io dtype; g, dg [B,H,L,D] f32; h0, hT, dhT, dh0 [B,H,D] f32.
+ * g may be any real (GLA_SCAN_NORM: g <= 0, where m is real; g = 0 there gives m = 0, whose
+ *   infinite slope is taken as 0). g = -inf is allowed: alpha = 0, so that token starts anew (a
+ *   packed document's first token). NaN and infinities in x, g or h0 spread as the formula says;
+ *   0 * inf is NaN, so a non-finite state passes through such a start too.
+ * Sums run in fp32. Nothing in the library's results depends on timing: the order of each
+ * channel's products is fixed by the problem's sizes. No atomics.
+ * gla_scan_fwd: o [B,H,L,D] (written) and hT (NULL: not written). L = 0 copies h0 (or zero) to hT.
+ * gla_scan_bwd: gradients of sum(dO * o) + sum(dhT * hT): dx, dg (written), dh0 (NULL: not
+ *   written); dhT NULL means 0. It recomputes the states in fp32.
+ * gla_scan_fwd_save / gla_scan_bwd_saved: the training pair; the forward leaves the state entering
+ *   every 64 tokens in `saved` (gla_scan_saved_bytes(p) bytes, caller-owned, NULL: not written),
+ *   the backward reads them instead of running the recurrence once more. `saved` must come from
+ *   gla_scan_fwd_save with the same problem, input and x, g, h0; NULL means recompute (the same
+ *   as gla_scan_bwd).
+ * ws: caller-owned device workspace of gla_scan_workspace_bytes(p, for_backward) bytes (0 when p
+ *   is invalid or unsupported). There is no device status word in it; the kernels' waits on their
+ *   own copies are bounded, and one that gave up leaves outputs unwritten rather than hanging.
+ * Outputs may not overlap inputs, saved or ws. All pointers 16-byte aligned device memory.
+ * Errors: GLA_ERR_INVALID_ARG (null or misaligned pointer, bad enum, sizes, a gate mode),
+ *   GLA_ERR_UNSUPPORTED (D, B * H), GLA_ERR_WORKSPACE, GLA_ERR_CUDA. */
+typedef enum {
+    GLA_SCAN_PLAIN = 0,      /* m = 1 */
+    GLA_SCAN_COMPLEMENT = 1, /* m = 1 - alpha */
+    GLA_SCAN_NORM = 2        /* m = sqrt(1 - alpha^2) */
+} gla_scan_input;
+GLA_API size_t gla_scan_workspace_bytes(const gla_problem* p, int for_backward);
+GLA_API size_t gla_scan_saved_bytes(const gla_problem* p);
+GLA_API gla_status gla_scan_fwd(const gla_problem* p, int input, const void* x, const float* g, const float* h0,
+                                void* o, float* hT, void* ws, size_t ws_bytes, void* stream);
+GLA_API gla_status gla_scan_bwd(const gla_problem* p, int input, const void* x, const float* g, const float* h0,
+                                const void* dO, const float* dhT, void* dx, float* dg, float* dh0, void* ws,
+                                size_t ws_bytes, void* stream);
+GLA_API gla_status gla_scan_fwd_save(const gla_problem* p, int input, const void* x, const float* g, const float* h0,
+                                     void* o, float* hT, float* saved, void* ws, size_t ws_bytes, void* stream);
+GLA_API gla_status gla_scan_bwd_saved(const gla_problem* p, int input, const void* x, const float* g,
+                                      const float* h0, const void* dO, const float* dhT, const float* saved,
+                                      void* dx, float* dg, float* dh0, void* ws, size_t ws_bytes, void* stream);
+
+/* One token of that recurrence from a given state, updated in place:
+ *     state <- alpha * state + m(alpha) * x,   o = state.
+ * p->L must be 1: x, o [B,H,1,D] io dtype, g [B,H,1,D] f32, state [B,H,D] f32 (read and
+ * overwritten; must not overlap the other buffers). The result equals gla_scan_fwd over the one
+ * token with h0 = state. No workspace. Errors: as gla_scan_fwd. */
+GLA_API gla_status gla_scan_decode(const gla_problem* p, int input, const void* x, const float* g, float* state,
+                                   void* o, void* stream);
+
+/* The norms before and after a block. */
+typedef enum {
+    GLA_NORM_RMS = 0,  /* n = r / sqrt(mean(r^2) + eps) */
+    GLA_NORM_LAYER = 1 /* n = (r - mean(r)) / sqrt(mean((r - mean(r))^2) + eps) */
+} gla_norm_kind;
+typedef enum {
+    GLA_ACT_SILU = 0,   /* act(z) = z / (1 + e^-z) */
+    GLA_ACT_SIGMOID = 1 /* act(z) = 1 / (1 + e^-z) */
+} gla_act;
+typedef struct {
+    int B, H, L, D;     /* gla_headnorm_*: batch, heads, tokens, channels of a head;
+                           gla_addnorm_*: B * L rows of D channels, H must be 1 */
+    gla_dtype io;       /* dtype of x, y, dx, dy (gla_addnorm_*), o, z, y and their gradients */
+    gla_dtype res;      /* gla_addnorm_*: dtype of res, r, dr, dres (GLA_F32, or io); ignored else */
+    int kind;           /* a gla_norm_kind */
+    int act;            /* gla_headnorm_*: a gla_act; ignored else */
+    int w_per_head;     /* gla_headnorm_*: w, dw are [H,D] (1) or [D], shared by the heads (0) */
+    float eps;          /* > 0, finite */
+    float alpha;        /* gla_addnorm_*: scale of the block's output; ignored else */
+} gla_norm_problem;
+
+/* Residual sum and the norm before the next block, over rows of D channels:
+ *     r = res + alpha * rscale * x,   y = norm(r) * w.
+ * x: the block's output; res: the residual stream (NULL: 0); rscale [D] f32: the learned scale of
+ * the block's output (NULL: 1); w [D] f32: the norm's weight (NULL: 1). r (NULL: not written; may
+ * be res itself) is written in p->res dtype, y in p->io dtype; y is the norm of the fp32 sum, not
+ * of the r that was rounded to be stored. Statistics run in fp32, the layer norm's variance about
+ * the mean.
+ * p: B, L >= 0, H = 1, 1 <= D <= 16384.
+ * gla_addnorm_bwd: gradients of sum(dy * y) + sum(dr * r), taken at the stored r:
+ *     dres = dr + d norm(r) (dy * w),  dx = alpha * rscale * dres,
+ *     dw = sum_rows dy * norm(r),  drscale = sum_rows alpha * x * dres.
+ *   r as gla_addnorm_fwd wrote it; dr (p->res dtype) the gradient that reaches r from later
+ *   blocks, NULL: 0; dres (p->res dtype; may be dr itself) and dx (p->io dtype) each NULL: not
+ *   written; dw, drscale [D] f32, NULL: not written; x is only read for drscale (else may be
+ *   NULL). drscale needs rscale. The row sums of dw and drscale are taken in a fixed order, without
+ *   atomics. Zero rows give dw = drscale = 0.
+ * ws: gla_addnorm_workspace_bytes(p) bytes of caller-owned device memory (0 when p is invalid or
+ *   unsupported), the backward's partial sums. Otherwise outputs may not overlap inputs or ws.
+ * All pointers 16-byte aligned device memory. Asynchronous on `stream`.
+ * Errors: GLA_ERR_INVALID_ARG (null or misaligned pointer, bad enum, size, eps), GLA_ERR_UNSUPPORTED
+ *   (D, dtypes), GLA_ERR_WORKSPACE, GLA_ERR_CUDA. */
+GLA_API size_t gla_addnorm_workspace_bytes(const gla_norm_problem* p);
+GLA_API gla_status gla_addnorm_fwd(const gla_norm_problem* p, const void* x, const void* res, const float* rscale,
+                                   const float* w, void* r, void* y, void* stream);
+GLA_API gla_status gla_addnorm_bwd(const gla_norm_problem* p, const void* x, const void* r, const float* rscale,
+                                   const float* w, const void* dy, const void* dr, void* dres, void* dx, float* dw,
+                                   float* drscale, void* ws, size_t ws_bytes, void* stream);
+
+/* Norm and gate after a cell, per head and token over the D channels of the head:
+ *     y = norm(o) * w * act(z),
+ * o [B,H,L,D] as the cells write it; z (the gate before its activation) and y [B,L,H,D], the
+ * layout of the projections around the block, so that y viewed as [B,L,H*D] is the
+ * out-projection's input. z NULL: no gate (act(z) = 1). w [D] or [H,D] f32 (p->w_per_head), NULL: 1.
+ * p: B, H, L >= 0, 1 <= D <= 16384, H <= 65535.
+ * gla_headnorm_bwd: gradients of sum(dy * y): d_o [B,H,L,D], dz [B,L,H,D] (written iff z is given;
+ *   NULL: not written), dw f32 shaped like w (NULL: not written), summed over rows in a fixed
+ *   order. dy [B,L,H,D].
+ * Workspace, aliasing and errors as for gla_addnorm_*. */
+GLA_API size_t gla_headnorm_workspace_bytes(const gla_norm_problem* p);
+GLA_API gla_status gla_headnorm_fwd(const gla_norm_problem* p, const void* o, const void* z, const float* w, void* y,
+                                    void* stream);
+GLA_API gla_status gla_headnorm_bwd(const gla_norm_problem* p, const void* o, const void* z, const float* w,
+                                    const void* dy, void* d_o, void* dz, float* dw, void* ws, size_t ws_bytes,
+                                    void* stream);
+
 /* Static description of a status code (never NULL). */
 GLA_API const char* gla_status_string(gla_status s);
 

@@ -15,6 +15,9 @@ GLA_OK, GLA_ERR_INVALID_ARG, GLA_ERR_UNSUPPORTED, GLA_ERR_WORKSPACE, GLA_ERR_CUD
 GLA_F32, GLA_BF16 = 0, 1
 GLA_GATE_NONE, GLA_GATE_PER_KEY, GLA_GATE_PER_HEAD = 0, 1, 2
 GLA_PLAN_AUTO, GLA_PLAN_SIMT, GLA_PLAN_TC = 0, 1, 2
+GLA_SCAN_PLAIN, GLA_SCAN_COMPLEMENT, GLA_SCAN_NORM = 0, 1, 2
+GLA_NORM_RMS, GLA_NORM_LAYER = 0, 1
+GLA_ACT_SILU, GLA_ACT_SIGMOID = 0, 1
 
 # Every symbol include/gla.h declares (checked by tests/test_abi_symbols.py).
 EXPORTED = ("gla_workspace_bytes", "gla_fwd", "gla_bwd", "gla_status_string",
@@ -24,7 +27,10 @@ EXPORTED = ("gla_workspace_bytes", "gla_fwd", "gla_bwd", "gla_status_string",
             "gla_decode", "gla_shard_state", "gla_state_fold", "gla_shard_state_grad", "gla_deltanet_fwd",
             "gla_deltanet_bwd_workspace_bytes", "gla_deltanet_bwd", "gla_mlstm_workspace_bytes", "gla_mlstm_fwd",
             "gla_mlstm_bwd", "gla_shard_workspace_bytes", "gla_deltanet_saved_bytes", "gla_deltanet_fwd_save",
-            "gla_deltanet_bwd_saved", "gla_mlstm_saved_bytes", "gla_mlstm_fwd_save", "gla_mlstm_bwd_saved")
+            "gla_deltanet_bwd_saved", "gla_mlstm_saved_bytes", "gla_mlstm_fwd_save", "gla_mlstm_bwd_saved",
+            "gla_scan_workspace_bytes", "gla_scan_saved_bytes", "gla_scan_fwd", "gla_scan_bwd", "gla_scan_fwd_save",
+            "gla_scan_bwd_saved", "gla_scan_decode", "gla_addnorm_workspace_bytes", "gla_addnorm_fwd",
+            "gla_addnorm_bwd", "gla_headnorm_workspace_bytes", "gla_headnorm_fwd", "gla_headnorm_bwd")
 
 
 class GlaProblem(ctypes.Structure):
@@ -32,6 +38,12 @@ class GlaProblem(ctypes.Structure):
                 ("Dk", ctypes.c_int), ("Dv", ctypes.c_int), ("chunk", ctypes.c_int),
                 ("scale", ctypes.c_float), ("io", ctypes.c_int), ("gate", ctypes.c_int),
                 ("plan", ctypes.c_int)]
+
+
+class GlaNormProblem(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("L", ctypes.c_int), ("D", ctypes.c_int),
+                ("io", ctypes.c_int), ("res", ctypes.c_int), ("kind", ctypes.c_int), ("act", ctypes.c_int),
+                ("w_per_head", ctypes.c_int), ("eps", ctypes.c_float), ("alpha", ctypes.c_float)]
 
 
 class GlaError(RuntimeError):
@@ -109,6 +121,27 @@ def _load():
     lib.gla_mlstm_fwd_save.restype = ctypes.c_int
     lib.gla_mlstm_bwd_saved.argtypes = [pp] + [ctypes.c_void_p] * 13 + [ctypes.c_size_t, ctypes.c_void_p]
     lib.gla_mlstm_bwd_saved.restype = ctypes.c_int
+    np_ = ctypes.POINTER(GlaNormProblem)
+    lib.gla_scan_workspace_bytes.argtypes = [pp, ctypes.c_int]
+    lib.gla_scan_workspace_bytes.restype = ctypes.c_size_t
+    lib.gla_scan_saved_bytes.argtypes = [pp]
+    lib.gla_scan_saved_bytes.restype = ctypes.c_size_t
+    lib.gla_scan_fwd.argtypes = [pp, ctypes.c_int] + [ctypes.c_void_p] * 6 + [ctypes.c_size_t, ctypes.c_void_p]
+    lib.gla_scan_bwd.argtypes = [pp, ctypes.c_int] + [ctypes.c_void_p] * 9 + [ctypes.c_size_t, ctypes.c_void_p]
+    lib.gla_scan_fwd_save.argtypes = [pp, ctypes.c_int] + [ctypes.c_void_p] * 7 + [ctypes.c_size_t, ctypes.c_void_p]
+    lib.gla_scan_bwd_saved.argtypes = [pp, ctypes.c_int] + [ctypes.c_void_p] * 10 + [ctypes.c_size_t, ctypes.c_void_p]
+    lib.gla_scan_decode.argtypes = [pp, ctypes.c_int] + [ctypes.c_void_p] * 5
+    lib.gla_addnorm_workspace_bytes.argtypes = [np_]
+    lib.gla_addnorm_workspace_bytes.restype = ctypes.c_size_t
+    lib.gla_addnorm_fwd.argtypes = [np_] + [ctypes.c_void_p] * 7
+    lib.gla_addnorm_bwd.argtypes = [np_] + [ctypes.c_void_p] * 11 + [ctypes.c_size_t, ctypes.c_void_p]
+    lib.gla_headnorm_workspace_bytes.argtypes = [np_]
+    lib.gla_headnorm_workspace_bytes.restype = ctypes.c_size_t
+    lib.gla_headnorm_fwd.argtypes = [np_] + [ctypes.c_void_p] * 5
+    lib.gla_headnorm_bwd.argtypes = [np_] + [ctypes.c_void_p] * 8 + [ctypes.c_size_t, ctypes.c_void_p]
+    for f in ("scan_fwd", "scan_bwd", "scan_fwd_save", "scan_bwd_saved", "scan_decode", "addnorm_fwd", "addnorm_bwd",
+              "headnorm_fwd", "headnorm_bwd"):
+        getattr(lib, "gla_" + f).restype = ctypes.c_int
     lib.gla_state_fold.argtypes = [pp, ctypes.c_int] + [ctypes.c_void_p] * 5
     lib.gla_state_fold.restype = ctypes.c_int
     lib.gla_decode.argtypes = [pp] + [ctypes.c_void_p] * 8

@@ -16,9 +16,12 @@ from typing import Dict, Optional, Tuple
 import torch
 
 from . import _lib
-from ._lib import GlaError, GlaProblem
+from ._lib import GlaError, GlaNormProblem, GlaProblem
 
 _PLANS = {"auto": _lib.GLA_PLAN_AUTO, "simt": _lib.GLA_PLAN_SIMT, "tc": _lib.GLA_PLAN_TC}
+_SCAN_INPUTS = {"plain": _lib.GLA_SCAN_PLAIN, "complement": _lib.GLA_SCAN_COMPLEMENT, "norm": _lib.GLA_SCAN_NORM}
+_NORM_KINDS = {"rms": _lib.GLA_NORM_RMS, "layer": _lib.GLA_NORM_LAYER}
+_ACTS = {"silu": _lib.GLA_ACT_SILU, "sigmoid": _lib.GLA_ACT_SIGMOID}
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -294,6 +297,281 @@ def gla_deltanet_bwd(q, k, v, beta, h0, dO, dhT=None, *, scale: Optional[float] 
     if host:
         names = list(out)
         out = dict(zip(names, _to_host([out[n] for n in names])))
+    return out
+
+
+def _take(name, t, shape, dtype, device):
+    """A checked argument on `device`: `shape` and `dtype` exactly, contiguous, or None."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    if t.device != device:
+        if t.device.type == "cuda":
+            raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
+        t = t.to(device, non_blocking=True)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t
+
+
+def _choice(name, value, table):
+    if value not in table:
+        raise ValueError(f"{name} must be one of {sorted(table)}")
+    return table[value]
+
+
+def _call(fn, device, *args):
+    """Launches on the current stream of `device`, with that device current."""
+    if device.index == torch.cuda.current_device():
+        return fn(*args, _stream_handle(device))
+    with torch.cuda.device(device):
+        return fn(*args, _stream_handle(device))
+
+
+def _device_of(t):
+    return torch.device("cuda", torch.cuda.current_device()) if t.device.type != "cuda" else t.device
+
+
+def make_scan_problem(x: torch.Tensor) -> GlaProblem:
+    """The gla_problem of the vector-state recurrence over x [B,H,L,D]."""
+    if x.dim() != 4:
+        raise ValueError("x must be [B, H, L, D]")
+    B, H, L, D = x.shape
+    return GlaProblem(B, H, L, D, D, 64, 1.0, _io_dtype(x.dtype), _lib.GLA_GATE_PER_KEY, _lib.GLA_PLAN_AUTO)
+
+
+def gla_scan_saved_bytes(problem: GlaProblem) -> int:
+    return int(_lib.lib.gla_scan_saved_bytes(ctypes.byref(problem)))
+
+
+def gla_scan_workspace_bytes(problem: GlaProblem, for_backward: bool) -> int:
+    return int(_lib.lib.gla_scan_workspace_bytes(ctypes.byref(problem), int(for_backward)))
+
+
+def _buffer(name, t, nbytes, device):
+    """A workspace or saved-states buffer of the caller, checked."""
+    if t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor on {device}")
+    if t.numel() * t.element_size() < nbytes:
+        raise GlaError(_lib.GLA_ERR_WORKSPACE, name)
+    return t
+
+
+def _work_buffer(workspace, nbytes, device, where):
+    if nbytes == 0:
+        raise GlaError(_lib.GLA_ERR_UNSUPPORTED, where)
+    if workspace is not None:
+        return _buffer("workspace", workspace, nbytes, device)
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def gla_scan_fwd(x, g, h0=None, *, input: str = "plain", output_final_state: bool = True,
+                 workspace: Optional[torch.Tensor] = None,
+                 saved_states: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Gated linear recurrence with a vector state, h_t = e^{g_t} h_{t-1} + m(g_t) x_t per channel:
+    x [B,H,L,D] (bf16 or fp32), g [B,H,L,D] fp32 (log-decay; -inf starts anew), h0 [B,H,D] fp32 or
+    None (zero). input picks m: "plain" 1, "complement" 1 - e^g, "norm" sqrt(1 - e^{2g}). Returns
+    o [B,H,L,D] (every h_t) and hT [B,H,D] fp32 (or None when output_final_state is False).
+    saved_states: optional device buffer (at least gla_scan_saved_bytes) that receives the states
+    entering every 64 tokens, for gla_scan_bwd(..., saved_states=). Host tensors are copied to the
+    current device and the results back."""
+    host, device = x.device.type != "cuda", _device_of(x)
+    prob, mode = make_scan_problem(x), _choice("input", input, _SCAN_INPUTS)
+    x = _take("x", x, x.shape, x.dtype, device)
+    g = _take("g", g, x.shape, torch.float32, device)
+    if g is None:
+        raise ValueError("g is needed")
+    ends = x.shape[:2] + x.shape[3:]
+    h0 = _take("h0", h0, ends, torch.float32, device)
+    ws = _work_buffer(workspace, gla_scan_workspace_bytes(prob, False), device, "gla_scan_workspace_bytes")
+    if saved_states is not None:
+        _buffer("saved_states", saved_states, gla_scan_saved_bytes(prob), device)
+    o = torch.empty_like(x)
+    hT = torch.empty(ends, dtype=torch.float32, device=device) if output_final_state else None
+    st = _call(_lib.lib.gla_scan_fwd_save, device, ctypes.byref(prob), mode, _ptr(x), _ptr(g), _ptr(h0), _ptr(o),
+               _ptr(hT), _ptr(saved_states), _ptr(ws), ws.numel() * ws.element_size())
+    _check(st, "gla_scan_fwd")
+    if host:
+        o, hT = _to_host([o, hT])
+    return o, hT
+
+
+def gla_scan_bwd(x, g, h0, dO, dhT=None, *, input: str = "plain", output_dh0: bool = True,
+                 workspace: Optional[torch.Tensor] = None,
+                 saved_states: Optional[torch.Tensor] = None) -> Dict[str, Optional[torch.Tensor]]:
+    """Gradients of sum(dO * o) + sum(dhT * hT) of gla_scan_fwd: dict dx (io dtype), dg (fp32) and
+    dh0 (fp32, or None when output_dh0 is False). saved_states: the buffer a gla_scan_fwd on the
+    same x, g, h0 and input filled, or None to run the recurrence again."""
+    host, device = x.device.type != "cuda", _device_of(x)
+    prob, mode = make_scan_problem(x), _choice("input", input, _SCAN_INPUTS)
+    x = _take("x", x, x.shape, x.dtype, device)
+    g = _take("g", g, x.shape, torch.float32, device)
+    dO = _take("dO", dO, x.shape, x.dtype, device)
+    if g is None or dO is None:
+        raise ValueError("g and dO are needed")
+    ends = x.shape[:2] + x.shape[3:]
+    h0 = _take("h0", h0, ends, torch.float32, device)
+    dhT = _take("dhT", dhT, ends, torch.float32, device)
+    ws = _work_buffer(workspace, gla_scan_workspace_bytes(prob, True), device, "gla_scan_workspace_bytes")
+    if saved_states is not None:
+        _buffer("saved_states", saved_states, gla_scan_saved_bytes(prob), device)
+    dx, dg = torch.empty_like(x), torch.empty_like(g)
+    dh0 = torch.empty(ends, dtype=torch.float32, device=device) if output_dh0 else None
+    st = _call(_lib.lib.gla_scan_bwd_saved, device, ctypes.byref(prob), mode, _ptr(x), _ptr(g), _ptr(h0), _ptr(dO),
+               _ptr(dhT), _ptr(saved_states), _ptr(dx), _ptr(dg), _ptr(dh0), _ptr(ws),
+               ws.numel() * ws.element_size())
+    _check(st, "gla_scan_bwd")
+    if host:
+        dx, dg, dh0 = _to_host([dx, dg, dh0])
+    return {"dx": dx, "dg": dg, "dh0": dh0}
+
+
+def gla_scan_decode(x, g, state, *, input: str = "plain") -> torch.Tensor:
+    """One token of gla_scan_fwd per (b, h) from `state` (fp32 [B,H,D] on the GPU, updated in
+    place): x, g [B,H,1,D]. Returns o [B,H,1,D]."""
+    if state.device.type != "cuda" or state.dtype != torch.float32 or not state.is_contiguous():
+        raise ValueError("state must be a contiguous float32 CUDA tensor (it is updated in place)")
+    device = state.device
+    prob, mode = make_scan_problem(x), _choice("input", input, _SCAN_INPUTS)
+    if x.shape[2] != 1:
+        raise ValueError("gla_scan_decode takes one token per (b, h): x must be [B, H, 1, D]")
+    x = _take("x", x, x.shape, x.dtype, device)
+    g = _take("g", g, x.shape, torch.float32, device)
+    if g is None:
+        raise ValueError("g is needed")
+    _take("state", state, x.shape[:2] + x.shape[3:], torch.float32, device)
+    o = torch.empty_like(x)
+    st = _call(_lib.lib.gla_scan_decode, device, ctypes.byref(prob), mode, _ptr(x), _ptr(g), _ptr(state), _ptr(o))
+    _check(st, "gla_scan_decode")
+    return o
+
+
+def _addnorm_problem(x, res_dtype, kind, eps, alpha) -> GlaNormProblem:
+    if x.dim() < 1:
+        raise ValueError("x must be [..., D]")
+    D = x.shape[-1]
+    if D < 1:
+        raise ValueError("x must have channels")
+    if x.numel() // D > 2147483647:
+        raise GlaError(_lib.GLA_ERR_UNSUPPORTED, "rows")
+    return GlaNormProblem(1, 1, x.numel() // D, D, _io_dtype(x.dtype), _io_dtype(res_dtype),
+                          _choice("kind", kind, _NORM_KINDS), _lib.GLA_ACT_SILU, 0, float(eps), float(alpha))
+
+
+def gla_addnorm_fwd(x, res=None, w=None, *, rscale=None, alpha: float = 1.0, kind: str = "rms", eps: float = 1e-6,
+                    res_dtype: Optional[torch.dtype] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Residual sum and norm before a block: r = res + alpha * rscale * x, y = norm(r) * w.
+    x [..., D] (bf16 or fp32) is the last block's output; res [..., D] the residual stream, of
+    x's dtype or fp32 (None: zero, with r in res_dtype, x's by default); w, rscale [D] fp32 or
+    None (one); kind "rms" or "layer". Returns r (res's dtype) and y (x's dtype); y is the norm of
+    the fp32 sum, before r is rounded. Host tensors are copied to the current device and the
+    results back."""
+    host, device = x.device.type != "cuda", _device_of(x)
+    if res is not None and res_dtype not in (None, res.dtype):
+        raise ValueError("res_dtype is res's dtype when res is given")
+    res_dtype = res.dtype if res is not None else (res_dtype or x.dtype)
+    prob = _addnorm_problem(x, res_dtype, kind, eps, alpha)
+    x = _take("x", x, x.shape, x.dtype, device)
+    res = _take("res", res, x.shape, res_dtype, device)
+    w = _take("w", w, x.shape[-1:], torch.float32, device)
+    rscale = _take("rscale", rscale, x.shape[-1:], torch.float32, device)
+    r, y = torch.empty(x.shape, dtype=res_dtype, device=device), torch.empty_like(x)
+    st = _call(_lib.lib.gla_addnorm_fwd, device, ctypes.byref(prob), _ptr(x), _ptr(res), _ptr(rscale), _ptr(w),
+               _ptr(r), _ptr(y))
+    _check(st, "gla_addnorm_fwd")
+    if host:
+        r, y = _to_host([r, y])
+    return r, y
+
+
+def gla_addnorm_bwd(x, r, w, dy, dr=None, *, rscale=None, alpha: float = 1.0, kind: str = "rms", eps: float = 1e-6,
+                    output_dx: bool = True, workspace: Optional[torch.Tensor] = None) -> Dict[str, Optional[torch.Tensor]]:
+    """Gradients of sum(dy * y) + sum(dr * r) of gla_addnorm_fwd at the r it returned: dict dres
+    (r's dtype), dx (dy's dtype; None when output_dx is False: with alpha = 1, no rscale and one
+    dtype it equals dres), dw (fp32 [D], None without w) and drscale (fp32 [D], None without
+    rscale). x is only read for drscale and may be None without rscale; dr [..., D] is the
+    gradient that reaches r from later blocks, or None."""
+    host, device = dy.device.type != "cuda", _device_of(dy)
+    prob = _addnorm_problem(dy, r.dtype, kind, eps, alpha)
+    D = dy.shape[-1:]
+    dy = _take("dy", dy, dy.shape, dy.dtype, device)
+    r = _take("r", r, dy.shape, r.dtype, device)
+    dr = _take("dr", dr, dy.shape, r.dtype, device)
+    w = _take("w", w, D, torch.float32, device)
+    rscale = _take("rscale", rscale, D, torch.float32, device)
+    if rscale is not None and x is None:
+        raise ValueError("x is needed for rscale's gradient")
+    x = _take("x", x, dy.shape, dy.dtype, device) if rscale is not None else None
+    ws = _work_buffer(workspace, int(_lib.lib.gla_addnorm_workspace_bytes(ctypes.byref(prob))), device,
+                      "gla_addnorm_workspace_bytes")
+    dres = torch.empty_like(r)
+    dx = torch.empty_like(dy) if output_dx else None
+    dw = torch.empty_like(w) if w is not None else None
+    ds = torch.empty_like(rscale) if rscale is not None else None
+    st = _call(_lib.lib.gla_addnorm_bwd, device, ctypes.byref(prob), _ptr(x), _ptr(r), _ptr(rscale), _ptr(w),
+               _ptr(dy), _ptr(dr), _ptr(dres), _ptr(dx), _ptr(dw), _ptr(ds), _ptr(ws),
+               ws.numel() * ws.element_size())
+    _check(st, "gla_addnorm_bwd")
+    out = {"dres": dres, "dx": dx, "dw": dw, "drscale": ds}
+    if host:
+        out = dict(zip(out, _to_host(list(out.values()))))
+    return out
+
+
+def _headnorm_problem(o, w, act, kind, eps) -> GlaNormProblem:
+    if o.dim() != 4:
+        raise ValueError("o must be [B, H, L, D]")
+    B, H, L, D = o.shape
+    per_head = 1 if w is not None and w.dim() == 2 else 0
+    return GlaNormProblem(B, H, L, D, _io_dtype(o.dtype), _io_dtype(o.dtype), _choice("kind", kind, _NORM_KINDS),
+                          _choice("act", act, _ACTS), per_head, float(eps), 1.0)
+
+
+def gla_headnorm_fwd(o, z=None, w=None, *, act: str = "silu", kind: str = "rms", eps: float = 1e-6) -> torch.Tensor:
+    """Norm and gate after a cell: y = norm(o) * w * act(z), normalised over the D channels of each
+    head and token. o [B,H,L,D] (bf16 or fp32) as the cells return it; z [B,L,H,D] the gate before
+    act ("silu" or "sigmoid"), None: no gate; w fp32 [D] (shared by the heads) or [H,D], None: one;
+    kind "rms" or "layer". Returns y [B,L,H,D]: y.view(B, L, H * D) is the out-projection's input.
+    Host tensors are copied to the current device and the result back."""
+    host, device = o.device.type != "cuda", _device_of(o)
+    prob = _headnorm_problem(o, w, act, kind, eps)
+    o = _take("o", o, o.shape, o.dtype, device)
+    B, H, L, D = o.shape
+    z = _take("z", z, torch.Size((B, L, H, D)), o.dtype, device)
+    w = _take("w", w, torch.Size((H, D) if prob.w_per_head else (D,)), torch.float32, device)
+    y = torch.empty(B, L, H, D, dtype=o.dtype, device=device)
+    st = _call(_lib.lib.gla_headnorm_fwd, device, ctypes.byref(prob), _ptr(o), _ptr(z), _ptr(w), _ptr(y))
+    _check(st, "gla_headnorm_fwd")
+    if host:
+        (y,) = _to_host([y])
+    return y
+
+
+def gla_headnorm_bwd(o, z, w, dy, *, act: str = "silu", kind: str = "rms", eps: float = 1e-6,
+                     workspace: Optional[torch.Tensor] = None) -> Dict[str, Optional[torch.Tensor]]:
+    """Gradients of sum(dy * y) of gla_headnorm_fwd: dict do [B,H,L,D], dz [B,L,H,D] (None without
+    z), dw (fp32, shaped like w; None without w)."""
+    host, device = o.device.type != "cuda", _device_of(o)
+    prob = _headnorm_problem(o, w, act, kind, eps)
+    o = _take("o", o, o.shape, o.dtype, device)
+    B, H, L, D = o.shape
+    z = _take("z", z, torch.Size((B, L, H, D)), o.dtype, device)
+    dy = _take("dy", dy, torch.Size((B, L, H, D)), o.dtype, device)
+    if dy is None:
+        raise ValueError("dy is needed")
+    w = _take("w", w, torch.Size((H, D) if prob.w_per_head else (D,)), torch.float32, device)
+    ws = _work_buffer(workspace, int(_lib.lib.gla_headnorm_workspace_bytes(ctypes.byref(prob))), device,
+                      "gla_headnorm_workspace_bytes")
+    d_o = torch.empty_like(o)
+    dz = torch.empty_like(z) if z is not None else None
+    dw = torch.empty_like(w) if w is not None else None
+    st = _call(_lib.lib.gla_headnorm_bwd, device, ctypes.byref(prob), _ptr(o), _ptr(z), _ptr(w), _ptr(dy), _ptr(d_o),
+               _ptr(dz), _ptr(dw), _ptr(ws), ws.numel() * ws.element_size())
+    _check(st, "gla_headnorm_bwd")
+    out = {"do": d_o, "dz": dz, "dw": dw}
+    if host:
+        out = dict(zip(out, _to_host(list(out.values()))))
     return out
 
 
