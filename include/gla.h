@@ -321,7 +321,7 @@ GLA_API gla_status gla_mlstm_bwd_saved(const gla_problem* p, const void* q, cons
  * elementwise, from h_{-1} = h0 (or 0), with h_{L-1} = hT. `input` is a gla_scan_input and picks
  * the factor m on the input: 1; 1 - alpha (a convex mix of state and input); or
  * sqrt(1 - alpha^2) (the state keeps the input's variance).
- * p: B, H, L >= 0; Dk = Dv = D, the channels per head, 1 <= D <= 65536; io; gate must be
+ * p: B, H, L >= 0; at most 2^30 tokens; Dk = Dv = D, the channels per head, 1 <= D <= 65536; io; gate must be
  *   GLA_GATE_PER_KEY; chunk, scale and plan are ignored.
  * x, o, dO, dx [B,H,L,D] in io dtype; g, dg [B,H,L,D] f32; h0, hT, dhT, dh0 [B,H,D] f32.
  * g may be any real (GLA_SCAN_NORM: g <= 0, where m is real; g = 0 there gives m = 0, whose
@@ -340,10 +340,11 @@ GLA_API gla_status gla_mlstm_bwd_saved(const gla_problem* p, const void* q, cons
  *   as gla_scan_bwd).
  * ws: caller-owned device workspace of gla_scan_workspace_bytes(p, for_backward) bytes (0 when p
  *   is invalid or unsupported). There is no device status word in it; the kernels' waits on their
- *   own copies are bounded, and one that gave up leaves outputs unwritten rather than hanging.
+ *   own copies are bounded, and one that gave up (a fault elsewhere on the device) ends the call
+ *   with results that are not valid rather than hanging.
  * Outputs may not overlap inputs, saved or ws. All pointers 16-byte aligned device memory.
  * Errors: GLA_ERR_INVALID_ARG (null or misaligned pointer, bad enum, sizes, a gate mode),
- *   GLA_ERR_UNSUPPORTED (D, B * H), GLA_ERR_WORKSPACE, GLA_ERR_CUDA. */
+ *   GLA_ERR_UNSUPPORTED (D, L, B * H), GLA_ERR_WORKSPACE, GLA_ERR_CUDA. */
 typedef enum {
     GLA_SCAN_PLAIN = 0,      /* m = 1 */
     GLA_SCAN_COMPLEMENT = 1, /* m = 1 - alpha */
