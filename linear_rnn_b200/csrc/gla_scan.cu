@@ -26,142 +26,159 @@ namespace {
 using namespace sm100;
 
 constexpr int kSaveEvery = 64;   // tokens between two saved states
-constexpr int NT_S = 256;        // threads of a tile
-constexpr int NW = NT_S / 32;
-constexpr int VEC = 4;           // channels of a thread
+constexpr int NW = 8;            // warps that hold a tile's tokens
+constexpr int VEC = 4;           // channels of a thread, two packed pairs
+constexpr int CHL = 8;           // lanes along the channels
+constexpr int CH = CHL * VEC;    // channels of a tile: 128-byte rows of g
 constexpr int RUN = 4;           // tokens of a thread
+constexpr int RW = 32 / CHL;     // runs of a warp
+constexpr int WT = RW * RUN;     // tokens of a warp
+constexpr int TT = NW * WT;      // tokens of a tile
+constexpr int ELEMS = TT * CH;
 constexpr int kMaxCluster = 8;
-constexpr int kMaxStages = 4;
+constexpr int kFwdStages = 3;    // tiles of the forward's ring
 
 // How a tile reaches shared memory.
 enum { LOAD_TMA = 0, LOAD_VEC4 = 1, LOAD_ONE = 2 };
 
-// 1 - e^g and e^g. Near 0 (|g| < 0.35, where a gate's memory is long and an error in a is
-// multiplied by 1 / (1 - a)) 1 - e^g is its Taylor series through g^7 / 7! (first term left out:
-// g^7 / 8! < 1.7e-8 of the value), and a = 1 - t is then exact to one rounding; elsewhere the
-// hardware exponential serves.
-__device__ __forceinline__ void gate(float g, float& a, float& t) {
-    float s = fmaf(g, 1.f / 5040.f, 1.f / 720.f);
-    s = fmaf(g, s, 1.f / 120.f);
-    s = fmaf(g, s, 1.f / 24.f);
-    s = fmaf(g, s, 1.f / 6.f);
-    s = fmaf(g, s, 0.5f);
-    s = fmaf(g, s, 1.f);
-    const float tn = -g * s, af = __expf(g);
-    const bool near = fabsf(g) < 0.35f;
-    t = near ? tn : 1.f - af;
-    a = near ? 1.f - tn : af;
+// ------------------------------------------------------------------ packed pairs of fp32
+using tc::f2;
+using tc::f2_fma;
+using tc::f2_mul;
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ void f2_split(uint64_t v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t f2_all(float v) { return f2(v, v); }
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rsqrt_approx(float x) {
+    float y;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
-// The factor on the input and its derivative with respect to g. u = 1 - a^2 = t (1 + a); u < 0
-// (g > 0) gives NaN like the formula.
+// a = e^g and t = 1 - e^g for two channels. For -0.30 <= g <= 0.05, where a gate's memory is long
+// and an error in a is multiplied by 1 / (1 - a), t = -g P(g) with P the degree-4 polynomial closest
+// to (e^g - 1) / g there with P(0) = 1 (least largest relative error, 2.2e-8), so t is within 2 and
+// a = 1 - t within 1.3 units of 2^-24; elsewhere the hardware exponential serves (2^-22).
+__device__ __forceinline__ void gate2(uint64_t g, uint64_t& a, uint64_t& t) {
+    uint64_t s = f2_fma(g, f2_all(-0.007552224211394787f), f2_all(-0.041534192860126495f));
+    s = f2_fma(g, s, f2_all(-0.1666625589132309f));
+    s = f2_fma(g, s, f2_all(-0.5000003576278687f));
+    s = f2_fma(g, s, f2_all(-1.f));
+    const uint64_t tn = f2_mul(g, s), an = f2_fma(tn, f2_all(-1.f), f2_all(1.f));
+    const uint64_t y = f2_mul(g, f2_all(1.4426950408889634f)), w = f2_add(g, f2_all(0.125f));
+    float y0, y1, w0, w1, a0, a1, t0, t1;
+    f2_split(y, y0, y1);
+    f2_split(w, w0, w1);
+    f2_split(an, a0, a1);
+    f2_split(tn, t0, t1);
+    const float e0 = ex2(y0), e1 = ex2(y1);
+    float q0, q1;
+    f2_split(f2_fma(f2(e0, e1), f2_all(-1.f), f2_all(1.f)), q0, q1);
+    const bool n0 = fabsf(w0) <= 0.175f, n1 = fabsf(w1) <= 0.175f;
+    a = f2(n0 ? a0 : e0, n1 ? a1 : e1);
+    t = f2(n0 ? t0 : q0, n1 ? t1 : q1);
+}
+
+// The factor on the input, from t. u = 1 - a^2 = t (2 - t); u < 0 (g > 0) gives NaN like the formula,
+// u below the normal numbers 0.
 template <int IN>
-__device__ __forceinline__ float in_factor(float t) {
-    if (IN == GLA_SCAN_PLAIN) return 1.f;
+__device__ __forceinline__ uint64_t in_factor2(uint64_t t) {
+    if (IN == GLA_SCAN_PLAIN) return f2_all(1.f);
     if (IN == GLA_SCAN_COMPLEMENT) return t;
-    const float u = t * (2.f - t);
-    return u == 0.f ? 0.f : u * rsqrtf(u);
+    float u0, u1;
+    f2_split(f2_mul(t, f2_fma(t, f2_all(-1.f), f2_all(2.f))), u0, u1);
+    const float m0 = u0 * rsqrt_approx(u0), m1 = u1 * rsqrt_approx(u1);
+    return f2(fabsf(u0) < 1.1754944e-38f ? 0.f : m0, fabsf(u1) < 1.1754944e-38f ? 0.f : m1);
 }
 template <int IN>
-__device__ __forceinline__ float in_slope(float a, float m) {
-    if (IN == GLA_SCAN_PLAIN) return 0.f;
-    if (IN == GLA_SCAN_COMPLEMENT) return -a;
-    return m == 0.f ? 0.f : __fdividef(-a * a, m);
+__device__ __forceinline__ uint64_t times_factor2(uint64_t m, uint64_t x) {
+    return IN == GLA_SCAN_PLAIN ? x : f2_mul(m, x);
+}
+// Its derivative with respect to g times x, plus c.
+template <int IN>
+__device__ __forceinline__ uint64_t slope_fma2(uint64_t a, uint64_t m, uint64_t x, uint64_t c) {
+    if (IN == GLA_SCAN_PLAIN) return c;
+    if (IN == GLA_SCAN_COMPLEMENT) return f2_fma(f2_mul(a, f2_all(-1.f)), x, c);
+    float m0, m1;
+    f2_split(m, m0, m1);
+    const float r0 = m0 == 0.f ? 0.f : -tc::rcp_approx(m0), r1 = m1 == 0.f ? 0.f : -tc::rcp_approx(m1);
+    return f2_fma(f2_mul(f2_mul(a, a), f2(r0, r1)), x, c);
 }
 
 // ------------------------------------------------------------------ four channels of a token
-__device__ __forceinline__ void lds4(const float* p, float (&v)[VEC]) {
-    const float4 f = *reinterpret_cast<const float4*>(p);
-    v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+__device__ __forceinline__ void ld4(const float* p, uint64_t (&v)[2]) {
+    const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(p);
+    v[0] = f.x;
+    v[1] = f.y;
 }
-__device__ __forceinline__ void lds4(const __nv_bfloat16* p, float (&v)[VEC]) {
+__device__ __forceinline__ void ld4(const __nv_bfloat16* p, uint64_t (&v)[2]) {
     const uint2 u = *reinterpret_cast<const uint2*>(p);
-    v[0] = __uint_as_float(u.x << 16); v[1] = __uint_as_float(u.x & 0xffff0000u);
-    v[2] = __uint_as_float(u.y << 16); v[3] = __uint_as_float(u.y & 0xffff0000u);
+    v[0] = f2(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u));
+    v[1] = f2(__uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
 }
-__device__ __forceinline__ void st4(float* p, const float (&v)[VEC]) {
-    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+__device__ __forceinline__ void st4(float* p, const uint64_t (&v)[2]) {
+    *reinterpret_cast<ulonglong2*>(p) = make_ulonglong2(v[0], v[1]);
 }
-__device__ __forceinline__ void st4(__nv_bfloat16* p, const float (&v)[VEC]) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
-    *reinterpret_cast<uint2*>(p) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+__device__ __forceinline__ uint32_t to_bf16x2(uint64_t v) {
+    float lo, hi;
+    f2_split(v, lo, hi);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&b);
+}
+__device__ __forceinline__ void st4(__nv_bfloat16* p, const uint64_t (&v)[2]) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(to_bf16x2(v[0]), to_bf16x2(v[1]));
 }
 // Stores the channels c .. c+3 that exist; whole vectors where D allows.
 template <int LOAD, typename T>
-__device__ __forceinline__ void put4(T* p, const float (&v)[VEC], int c, int D) {
+__device__ __forceinline__ void put4(T* p, const uint64_t (&v)[2], int c, int D) {
     if (LOAD != LOAD_ONE) {
         if (c < D) st4(p, v);
     } else {
+        float f[VEC];
+        f2_split(v[0], f[0], f[1]);
+        f2_split(v[1], f[2], f[3]);
 #pragma unroll
         for (int i = 0; i < VEC; ++i)
-            if (c + i < D) p[i] = from_f<T>(v[i]);
+            if (c + i < D) p[i] = from_f<T>(f[i]);
     }
 }
 
-// (A, B) of this CTA's tile into slot `dst` of the cluster's CTA `rank`, counted on its barrier.
+// Loads them the same way, zeros (the identity: a = 1, b = 0) where there are none.
+template <int LOAD, typename T>
+__device__ __forceinline__ void get4(const T* p, uint64_t (&v)[2], bool row, int c, int D) {
+    v[0] = v[1] = 0;
+    if (!row) return;
+    if (LOAD != LOAD_ONE) {
+        if (c < D) ld4(p, v);
+    } else {
+        float f[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) f[i] = c + i < D ? to_f(p[i]) : 0.f;
+        v[0] = f2(f[0], f[1]);
+        v[1] = f2(f[2], f[3]);
+    }
+}
+
+// A pair into shared memory of a CTA of the cluster, counted on that CTA's barrier.
 __device__ __forceinline__ void st_async_pair(uint32_t dst, uint32_t bar, float a, float b) {
     asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(dst),
                  "f"(a), "f"(b), "r"(bar)
                  : "memory");
 }
-
-// Geometry of a tile: CHL lanes cover CH channels, the other lanes and the warps split TT tokens.
-template <int CHL>
-struct Geo {
-    static constexpr int CH = CHL * VEC;
-    static constexpr int RW = 32 / CHL;          // runs of a warp
-    static constexpr int WT = RW * RUN;          // tokens of a warp
-    static constexpr int TT = NW * WT;           // tokens of a tile
-    static constexpr int ELEMS = TT * CH;
-};
-
-// Shared memory behind the ring: per-warp sums, per-warp start values, exchange slots, barriers.
-template <int CHL, int SUMS>
-struct Tail {
-    float sum[SUMS][NW][Geo<CHL>::CH];
-    float start[SUMS - 1][NW][Geo<CHL>::CH];
-    float2 slot[2][kMaxCluster][Geo<CHL>::CH];
-    uint64_t full[kMaxStages];
-    uint64_t got[2];
-};
-
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
-}
-
-// A tile's elements into shared memory by ordinary loads, zeros (the identity: a = 1, b = 0) outside.
-template <int CHL, int LOAD, typename T>
-__device__ __forceinline__ void fill(T* dst, const T* __restrict__ src, size_t bh, int t0, int c0, int L, int D) {
-    using G = Geo<CHL>;
-    if (LOAD == LOAD_VEC4) {
-        constexpr int N = G::ELEMS / VEC / NT_S;
-        float v[N][VEC];
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-            const int e = threadIdx.x + k * NT_S, t = e / CHL, c = (e % CHL) * VEC;
-            v[k][0] = v[k][1] = v[k][2] = v[k][3] = 0.f;
-            if (t0 + t < L && c0 + c < D) lds4(src + (bh * L + t0 + t) * D + c0 + c, v[k]);
-        }
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-            const int e = threadIdx.x + k * NT_S;
-            st4(dst + e * VEC, v[k]);
-        }
-    } else {
-        constexpr int N = G::ELEMS / NT_S;
-        T v[N];
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-            const int e = threadIdx.x + k * NT_S, t = e / G::CH, c = e % G::CH;
-            v[k] = from_f<T>(0.f);
-            if (t0 + t < L && c0 + c < D) v[k] = src[(bh * L + t0 + t) * D + c0 + c];
-        }
-#pragma unroll
-        for (int k = 0; k < N; ++k) dst[threadIdx.x + k * NT_S] = v[k];
-    }
 }
 
 struct ScanArgs {
@@ -169,95 +186,82 @@ struct ScanArgs {
     const float* g;
     const void* dO;
     const float* first;    // h0 (forward), dhT (backward); may be null
-    void* out;             // o, dx
+    void* out;             // o (may be null), dx
     float* dg;
     float* last;           // hT, dh0; may be null
     float* saved;          // written (forward, may be null), read (backward)
-    int L, D, nblk, steps, stages;
+    int L, D, nblk, steps;
 };
-
-// Inclusive composition over the runs of a warp, lanes CHL apart, from the first run on.
-template <int CHL>
-__device__ __forceinline__ void warp_compose_up(float (&A)[VEC], float (&B)[VEC], int run) {
-#pragma unroll
-    for (int off = CHL; off < 32; off <<= 1)
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            const float pa = __shfl_up_sync(0xffffffffu, A[i], off), pb = __shfl_up_sync(0xffffffffu, B[i], off);
-            if (run >= off / CHL) {
-                B[i] = fmaf(A[i], pb, B[i]);
-                A[i] *= pa;
-            }
-        }
-}
-// The same from the last run backwards.
-template <int CHL>
-__device__ __forceinline__ void warp_compose_down(float (&A)[VEC], float (&B)[VEC], int run) {
-#pragma unroll
-    for (int off = CHL; off < 32; off <<= 1)
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            const float pa = __shfl_down_sync(0xffffffffu, A[i], off), pb = __shfl_down_sync(0xffffffffu, B[i], off);
-            if (run + off / CHL < 32 / CHL) {
-                B[i] = fmaf(A[i], pb, B[i]);
-                A[i] *= pa;
-            }
-        }
-}
 
 // Sends (A, B) to every CTA of the cluster, waits for theirs and composes them onto `super` in
 // sequence order (reverse order for REV). Returns the value entering this CTA's tile; `super`
 // becomes the value leaving the row of tiles. Slots are used in turn, two rows of tiles apart: a
 // CTA writes row i + 2 only after it has seen every CTA's row i + 1, which each thread sends after
 // it has read its channel of row i.
-template <int CHL, bool REV, int SUMS>
-__device__ __forceinline__ float exchange(Tail<CHL, SUMS>& sm, int c, float A, float B, int cs, int rank, int i,
+template <bool REV, typename Tail>
+__device__ __forceinline__ float exchange(Tail& sm, int c, float A, float B, int cs, int rank, int i,
                                           float& super, bool& ok) {
+    float in = super;
     if (cs == 1) {
-        const float in = super;
         super = fmaf(A, super, B);
         return in;
     }
     const int p = i & 1;
-    if (c == 0) mbar_arrive_expect_tx(&sm.got[p], cs * Geo<CHL>::CH * (uint32_t)sizeof(float2));
+    if (c == 0) mbar_arrive_expect_tx(&sm.got[p], cs * CH * (uint32_t)sizeof(float2));
     for (int r = 0; r < cs; ++r)
-        st_async_pair(mapa_shared(&sm.slot[p][rank][c], r), mapa_shared(&sm.got[p], r), A, B);
+        st_async_pair(mapa_shared(&sm.slot[(p * cs + rank) * CH + c], r), mapa_shared(&sm.got[p], r), A, B);
     if (ok) ok = mbar_wait_cluster(&sm.got[p], (i >> 1) & 1);
-    float in = super;
     for (int k = 0; k < cs; ++k) {
         const int r = REV ? cs - 1 - k : k;
         if (r == rank) in = super;
-        const float2 v = sm.slot[p][r][c];
+        const float2 v = sm.slot[(p * cs + r) * CH + c];
         super = fmaf(v.x, super, v.y);
     }
     return in;
 }
 
+// Shared memory of the forward behind its ring: the runs' (A, B) of a tile, their start values, the
+// barriers, and (clusters only) the exchange slots [2][cs][CH].
+constexpr int RUNS = TT / RUN;
+constexpr int NT_F = 32 * NW + 64;   // + the warp that composes the runs, + the warp that loads
+struct FwdTail {
+    float A[RUNS][CH], B[RUNS][CH];
+    float start[RUNS][CH];
+    uint64_t full[kFwdStages], empty[kFwdStages];
+    uint64_t sums, starts;
+    uint64_t got[2];
+    float2 slot[1];   // as many as the launch asks for
+};
+
 // One cluster per (b, h, block of CH channels); its CTAs take the tiles of a row of tiles in
-// order and walk the rows together. Three phases a row, with a barrier after the first two:
-// (1) every thread composes its tokens, warps their runs; (2) one thread per channel composes the
-// warps and the cluster's tiles; (3) every thread walks its tokens again from its start value.
-// The ring of tiles hides the loads; phase 2 hides behind the SM's other CTAs.
-template <typename T, int IN, int CHL, int LOAD>
-__global__ void __launch_bounds__(NT_S, 3)
+// order and walk the rows together. Three kinds of warps, which meet only at shared-memory barriers:
+//   warps 0-7  compose their runs of tile i (keeping a, b in registers), hand (A, B) on, and then
+//              walk tile i - 1 from its start values to the outputs;
+//   warp 8     lane = channel: composes the runs and, across the cluster, the tiles, and hands the
+//              runs' start values back - behind the others' work on the next tile;
+//   warp 9     keeps the ring of tiles full.
+template <typename T, int IN, int LOAD>
+__global__ void __launch_bounds__(NT_F, 2)
     k_scan_fwd(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mg, const ScanArgs P,
                int cs) {
-    using G = Geo<CHL>;
     extern __shared__ __align__(128) uint8_t smem[];
-    constexpr int kStage = G::ELEMS * (4 + (int)sizeof(T));
-    Tail<CHL, 2>& sm = *reinterpret_cast<Tail<CHL, 2>*>(smem + P.stages * kStage);
+    constexpr int kStage = ELEMS * (4 + (int)sizeof(T));
+    FwdTail& sm = *reinterpret_cast<FwdTail*>(smem + (LOAD == LOAD_TMA ? kFwdStages * kStage : 0));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int run = lane / CHL, ch = (lane % CHL) * VEC;
     const int rank = cs > 1 ? (int)cluster_rank() : 0;
     const unsigned chain = blockIdx.x / cs;
     const size_t bh = chain / P.nblk;
-    const int c0 = (int)(chain % P.nblk) * G::CH;
-    const int tr = warp * G::WT + run * RUN;   // this thread's first token in a tile
+    const int c0 = (int)(chain % P.nblk) * CH;
     const int L = P.L, D = P.D;
     bool ok = true;   // false once a wait gave up: no further wait, the results are not valid
 
     if (tid == 0) {
-        for (int s = 0; s < kMaxStages; ++s) mbar_init(&sm.full[s], 1);
+        for (int s = 0; s < kFwdStages; ++s) {
+            mbar_init(&sm.full[s], 1);
+            mbar_init(&sm.empty[s], NW);
+        }
+        mbar_init(&sm.sums, NW);
+        mbar_init(&sm.starts, 1);
         mbar_init(&sm.got[0], 1);
         mbar_init(&sm.got[1], 1);
         mbar_fence_init();
@@ -265,122 +269,170 @@ __global__ void __launch_bounds__(NT_S, 3)
     if (cs > 1) cluster_sync();
     else __syncthreads();
 
-    auto load = [&](int i) {   // one thread
-        const int s = i % P.stages;
-        float* sg = reinterpret_cast<float*>(smem + s * kStage);
-        mbar_arrive_expect_tx(&sm.full[s], kStage);
-        tma_load_3d(sg, &mg, c0, (i * cs + rank) * G::TT, (int)bh, &sm.full[s]);
-        tma_load_3d(sg + G::ELEMS, &mx, c0, (i * cs + rank) * G::TT, (int)bh, &sm.full[s]);
-    };
-    if (LOAD == LOAD_TMA && tid == 0)
-        for (int i = 0; i < P.stages && i < P.steps; ++i) load(i);
+    if (warp < NW) {
+        const int run = warp * RW + lane / CHL, ch = (lane % CHL) * VEC;
+        const int tr = run * RUN;   // this thread's first token in a tile
+        const T* xg = static_cast<const T*>(P.x) + bh * L * D + c0 + ch;
+        const float* gg = P.g + bh * L * D + c0 + ch;
+        T* og = static_cast<T*>(P.out) + bh * L * D + c0 + ch;
 
-    float super = 0.f;
-    if (tid < G::CH && P.first && c0 + tid < D) super = P.first[bh * D + c0 + tid];
-
-    for (int i = 0; i < P.steps; ++i) {
-        const int s = LOAD == LOAD_TMA ? i % P.stages : 0, t0 = (i * cs + rank) * G::TT;
-        float* sg = reinterpret_cast<float*>(smem + s * kStage);
-        T* sx = reinterpret_cast<T*>(sg + G::ELEMS);
-        if (LOAD == LOAD_TMA) {
-            if (ok) ok = mbar_wait(&sm.full[s], (i / P.stages) & 1);
-        } else {
-            fill<CHL, LOAD>(sg, P.g, bh, t0, c0, L, D);
-            fill<CHL, LOAD>(sx, static_cast<const T*>(P.x), bh, t0, c0, L, D);
-            __syncthreads();
-        }
-        float a[RUN][VEC], b[RUN][VEC], A[VEC], B[VEC];
+        auto compose = [&](int i, uint64_t (&a)[RUN][2], uint64_t (&b)[RUN][2], uint64_t (&A)[2], uint64_t (&B)[2]) {
+            const int s = i % kFwdStages;
+            const float* sg = reinterpret_cast<const float*>(smem + s * kStage) + tr * CH + ch;
+            const T* sx = reinterpret_cast<const T*>(smem + s * kStage + ELEMS * 4) + tr * CH + ch;
+            const int t = (i * cs + rank) * TT + tr;
+            if (LOAD == LOAD_TMA && ok) ok = mbar_wait(&sm.full[s], (i / kFwdStages) & 1);
+            uint64_t gv[RUN][2], xv[RUN][2];
 #pragma unroll
-        for (int j = 0; j < RUN; ++j) {
-            float gv[VEC], xv[VEC];
-            lds4(sg + (tr + j) * G::CH + ch, gv);
-            lds4(sx + (tr + j) * G::CH + ch, xv);
-#pragma unroll
-            for (int k = 0; k < VEC; ++k) {
-                float u;
-                gate(gv[k], a[j][k], u);
-                b[j][k] = in_factor<IN>(u) * xv[k];
-                A[k] = j ? A[k] * a[j][k] : a[j][k];
-                B[k] = j ? fmaf(a[j][k], B[k], b[j][k]) : b[j][k];
+            for (int j = 0; j < RUN; ++j) {
+                if (LOAD == LOAD_TMA) {
+                    ld4(sg + j * CH, gv[j]);
+                    ld4(sx + j * CH, xv[j]);
+                } else {
+                    get4<LOAD>(gg + (size_t)(t + j) * D, gv[j], t + j < L, c0 + ch, D);
+                    get4<LOAD>(xg + (size_t)(t + j) * D, xv[j], t + j < L, c0 + ch, D);
+                }
             }
-        }
-        warp_compose_up<CHL>(A, B, run);
-        if (run == G::RW - 1) {
-            st4(&sm.sum[0][warp][ch], A);
-            st4(&sm.sum[1][warp][ch], B);
-        }
-        // what the warp's earlier runs do to the warp's start value
-        float eA[VEC], eB[VEC];
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) {
-            eA[k] = __shfl_up_sync(0xffffffffu, A[k], CHL);
-            eB[k] = __shfl_up_sync(0xffffffffu, B[k], CHL);
-            if (run == 0) eA[k] = 1.f, eB[k] = 0.f;
-        }
-        __syncthreads();
-        if (LOAD == LOAD_TMA && tid == 0 && i + P.stages < P.steps) load(i + P.stages);
-        if (tid < G::CH) {
-            float pA[NW], pB[NW], tA = 1.f, tB = 0.f;
+            for (int j = 0; j < RUN; ++j)
 #pragma unroll
-            for (int w = 0; w < NW; ++w) {
-                pA[w] = tA, pB[w] = tB;
-                const float wa = sm.sum[0][w][tid], wb = sm.sum[1][w][tid];
-                tB = fmaf(wa, tB, wb);
-                tA *= wa;
+                for (int k = 0; k < 2; ++k) {
+                    uint64_t u;
+                    gate2(gv[j][k], a[j][k], u);
+                    b[j][k] = times_factor2<IN>(in_factor2<IN>(u), xv[j][k]);
+                    A[k] = j ? f2_mul(A[k], a[j][k]) : a[j][k];
+                    B[k] = j ? f2_fma(a[j][k], B[k], b[j][k]) : b[j][k];
+                }
+            if (LOAD == LOAD_TMA) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.empty[s]);
             }
-            const float in = exchange<CHL, false>(sm, tid, tA, tB, cs, rank, i, super, ok);
-#pragma unroll
-            for (int w = 0; w < NW; ++w) {
-                const float h = fmaf(pA[w], in, pB[w]);
-                sm.start[0][w][tid] = h;
-                const int t = t0 + w * G::WT;
-                if (w * G::WT % kSaveEvery == 0 && P.saved && t < L && c0 + tid < D)
-                    P.saved[(bh * cdiv(L, kSaveEvery) + t / kSaveEvery) * D + c0 + tid] = h;
-            }
-        }
-        __syncthreads();
-        if (P.out) {
-            float h[VEC];
-            lds4(&sm.start[0][warp][ch], h);
-            T* op = static_cast<T*>(P.out) + (bh * L + t0 + tr) * D + c0 + ch;
-#pragma unroll
-            for (int k = 0; k < VEC; ++k) h[k] = fmaf(eA[k], h[k], eB[k]);
+        };
+        auto hand_on = [&](const uint64_t (&A)[2], const uint64_t (&B)[2]) {
+            st4(&sm.A[run][ch], A);
+            st4(&sm.B[run][ch], B);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.sums);
+        };
+        auto take_start = [&](int i, uint64_t (&h)[2]) {
+            if (ok) ok = mbar_wait(&sm.starts, i & 1);
+            ld4(&sm.start[run][ch], h);
+        };
+        auto finish = [&](int i, uint64_t (&h)[2], const uint64_t (&a)[RUN][2], const uint64_t (&b)[RUN][2]) {
+            if (!P.out) return;
+            const int t = (i * cs + rank) * TT + tr;
 #pragma unroll
             for (int j = 0; j < RUN; ++j) {
 #pragma unroll
-                for (int k = 0; k < VEC; ++k) h[k] = fmaf(a[j][k], h[k], b[j][k]);
-                if (t0 + tr + j < L) put4<LOAD>(op + (size_t)j * D, h, c0 + ch, D);
+                for (int k = 0; k < 2; ++k) h[k] = f2_fma(a[j][k], h[k], b[j][k]);
+                if (t + j < L) put4<LOAD>(og + (size_t)(t + j) * D, h, c0 + ch, D);
             }
+        };
+        // The runs' sums and start values have one buffer each: (A, B) of tile i are written after the
+        // start values of tile i - 1 are there (so its sums have been read) and have been read.
+        uint64_t a0[RUN][2], b0[RUN][2], a1[RUN][2], b1[RUN][2], A[2], B[2], h[2];
+        if (P.steps > 0) {
+            compose(0, a0, b0, A, B);
+            hand_on(A, B);
+        }
+        for (int i = 1; i <= P.steps; i += 2) {
+            if (i < P.steps) compose(i, a1, b1, A, B);
+            take_start(i - 1, h);
+            if (i < P.steps) hand_on(A, B);
+            finish(i - 1, h, a0, b0);
+            if (i == P.steps) break;
+            if (i + 1 < P.steps) compose(i + 1, a0, b0, A, B);
+            take_start(i, h);
+            if (i + 1 < P.steps) hand_on(A, B);
+            finish(i, h, a1, b1);
+        }
+    } else if (warp == NW) {
+        const bool live = c0 + lane < D;
+        float super = P.first && live ? P.first[bh * D + c0 + lane] : 0.f;
+        for (int i = 0; i < P.steps; ++i) {
+            const int t0 = (i * cs + rank) * TT;
+            if (ok) ok = mbar_wait(&sm.sums, i & 1);
+            float in = super;
+            if (cs > 1) {
+                float tA = 1.f, tB = 0.f;
+#pragma unroll
+                for (int r = 0; r < RUNS; ++r) {
+                    const float ra = sm.A[r][lane];
+                    tB = fmaf(ra, tB, sm.B[r][lane]);
+                    tA *= ra;
+                }
+                in = exchange<false>(sm, lane, tA, tB, cs, rank, i, super, ok);
+            }
+            float h = in;
+#pragma unroll
+            for (int r = 0; r < RUNS; ++r) {
+                sm.start[r][lane] = h;
+                const int t = t0 + r * RUN;
+                if (r * RUN % kSaveEvery == 0 && P.saved && t < L && live)
+                    P.saved[(bh * cdiv(L, kSaveEvery) + t / kSaveEvery) * D + c0 + lane] = h;
+                h = fmaf(sm.A[r][lane], h, sm.B[r][lane]);
+            }
+            if (cs == 1) super = h;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.starts);
+        }
+        if (P.last && rank == 0 && live) P.last[bh * D + c0 + lane] = super;
+    } else if (LOAD == LOAD_TMA && lane == 0) {
+        for (int i = 0; i < P.steps; ++i) {
+            const int s = i % kFwdStages, t0 = (i * cs + rank) * TT;
+            float* sg = reinterpret_cast<float*>(smem + s * kStage);
+            if (i >= kFwdStages && ok) ok = mbar_wait(&sm.empty[s], (i / kFwdStages - 1) & 1);
+            mbar_arrive_expect_tx(&sm.full[s], kStage);
+            tma_load_3d(sg, &mg, c0, t0, (int)bh, &sm.full[s]);
+            tma_load_3d(sg + ELEMS, &mx, c0, t0, (int)bh, &sm.full[s]);
         }
     }
-    if (P.last && rank == 0 && tid < G::CH && c0 + tid < D) P.last[bh * D + c0 + tid] = super;
+    __syncwarp();
     if (cs > 1) cluster_sync();   // no CTA leaves while another may still write to its slots
 }
 
-// The same walk from the sequence's end, with the states recomputed inside each tile from the saved
-// ones: phase 1 also composes the reverse recurrence, phase 2 starts the forward one from
-// the saved state of every 64 tokens and carries the reverse one through the cluster, and phase 3
-// walks forward for h_{t-1}, then backward for the gradients.
-template <typename T, int IN, int CHL, int LOAD>
-__global__ void __launch_bounds__(NT_S, 2)
+// Shared memory of the backward behind its ring. The composing warp replaces a run's B and R by the
+// state and the gradient that enter the run (from its first and last token).
+template <int STAGES>
+struct BwdTail {
+    float A[RUNS][CH], B[RUNS][CH], R[RUNS][CH];
+    uint64_t full[STAGES], empty[STAGES];
+    uint64_t sums, starts;
+    uint64_t got[2];
+    float2 slot[1];
+};
+// Tiles of the ring: two CTAs share an SM's 227 KB.
+template <typename T>
+constexpr int bwd_stages() { return sizeof(T) == 2 ? 3 : 2; }
+
+// The same walk from the sequence's end, by the same three kinds of warps. The states are
+// recomputed inside each tile from the saved ones of every 64 tokens. A tile stays in the ring until
+// its gradients are out: the walk to the gradients reads it again and forms the gates anew, which
+// costs less than the registers that would keep them (the ring is then free for the tile after next).
+template <typename T, int IN, int LOAD>
+__global__ void __launch_bounds__(NT_F, 2)
     k_scan_bwd(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mg,
                const __grid_constant__ CUtensorMap md, const ScanArgs P, int cs) {
-    using G = Geo<CHL>;
     extern __shared__ __align__(128) uint8_t smem[];
-    constexpr int kStage = G::ELEMS * (4 + 2 * (int)sizeof(T));
-    Tail<CHL, 3>& sm = *reinterpret_cast<Tail<CHL, 3>*>(smem + P.stages * kStage);
+    constexpr int kStage = ELEMS * (4 + 2 * (int)sizeof(T)), S = bwd_stages<T>();
+    BwdTail<S>& sm = *reinterpret_cast<BwdTail<S>*>(smem + (LOAD == LOAD_TMA ? S * kStage : 0));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int run = lane / CHL, ch = (lane % CHL) * VEC;
     const int rank = cs > 1 ? (int)cluster_rank() : 0;
     const unsigned chain = blockIdx.x / cs;
     const size_t bh = chain / P.nblk;
-    const int c0 = (int)(chain % P.nblk) * G::CH;
-    const int tr = warp * G::WT + run * RUN;
+    const int c0 = (int)(chain % P.nblk) * CH;
     const int L = P.L, D = P.D;
-    bool ok = true;   // false once a wait gave up: no further wait, the results are not valid
+    bool ok = true;
+    // rows are counted from the end: row i holds the tiles (steps - 1 - i) cs + rank
+    auto first_token = [&](int i) { return ((P.steps - 1 - i) * cs + rank) * TT; };
 
     if (tid == 0) {
-        for (int s = 0; s < kMaxStages; ++s) mbar_init(&sm.full[s], 1);
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&sm.full[s], 1);
+            mbar_init(&sm.empty[s], NW);
+        }
+        mbar_init(&sm.sums, NW);
+        mbar_init(&sm.starts, 1);
         mbar_init(&sm.got[0], 1);
         mbar_init(&sm.got[1], 1);
         mbar_fence_init();
@@ -388,151 +440,169 @@ __global__ void __launch_bounds__(NT_S, 2)
     if (cs > 1) cluster_sync();
     else __syncthreads();
 
-    // rows are counted from the end: row i holds the tiles (steps - 1 - i) cs + rank
-    auto load = [&](int i) {
-        const int s = i % P.stages, t0 = ((P.steps - 1 - i) * cs + rank) * G::TT;
-        float* sg = reinterpret_cast<float*>(smem + s * kStage);
-        T* sx = reinterpret_cast<T*>(sg + G::ELEMS);
-        mbar_arrive_expect_tx(&sm.full[s], kStage);
-        tma_load_3d(sg, &mg, c0, t0, (int)bh, &sm.full[s]);
-        tma_load_3d(sx, &mx, c0, t0, (int)bh, &sm.full[s]);
-        tma_load_3d(sx + G::ELEMS, &md, c0, t0, (int)bh, &sm.full[s]);
-    };
-    if (LOAD == LOAD_TMA && tid == 0)
-        for (int i = 0; i < P.stages - 1 && i < P.steps; ++i) load(i);
+    if (warp < NW) {
+        const int run = warp * RW + lane / CHL, ch = (lane % CHL) * VEC;
+        const int tr = run * RUN;
+        const size_t base = bh * L * D + c0 + ch;
+        const T *xg = static_cast<const T*>(P.x) + base, *dg = static_cast<const T*>(P.dO) + base;
+        const float* gg = P.g + base;
+        T* xo = static_cast<T*>(P.out) + base;
+        float* go = P.dg + base;
 
-    float super = 0.f;
-    if (tid < G::CH && P.first && c0 + tid < D) super = P.first[bh * D + c0 + tid];
-
-    for (int i = 0; i < P.steps; ++i) {
-        const int s = LOAD == LOAD_TMA ? i % P.stages : 0, t0 = ((P.steps - 1 - i) * cs + rank) * G::TT;
-        float* sg = reinterpret_cast<float*>(smem + s * kStage);
-        T* sx = reinterpret_cast<T*>(sg + G::ELEMS);
-        T* sd = sx + G::ELEMS;
-        constexpr int NS = G::TT / kSaveEvery;   // saved states of a tile
-        float sv[NS];
-        if (tid < G::CH)
+        // token j of this thread's run in the row's tile
+        auto read = [&](int s, int t, int j, uint64_t (&gv)[2], uint64_t (&xv)[2]) {
+            const float* sg = reinterpret_cast<const float*>(smem + s * kStage) + (tr + j) * CH + ch;
+            if (LOAD == LOAD_TMA) {
+                ld4(sg, gv);
+                ld4(reinterpret_cast<const T*>(smem + s * kStage + ELEMS * 4) + (tr + j) * CH + ch, xv);
+            } else {
+                get4<LOAD>(gg + (size_t)(t + j) * D, gv, t + j < L, c0 + ch, D);
+                get4<LOAD>(xg + (size_t)(t + j) * D, xv, t + j < L, c0 + ch, D);
+            }
+        };
+        auto read_d = [&](int s, int t, int j, uint64_t (&dv)[2]) {
+            if (LOAD == LOAD_TMA)
+                ld4(reinterpret_cast<const T*>(smem + s * kStage + ELEMS * (4 + sizeof(T))) + (tr + j) * CH + ch, dv);
+            else
+                get4<LOAD>(dg + (size_t)(t + j) * D, dv, t + j < L, c0 + ch, D);
+        };
+        auto compose = [&](int i, uint64_t (&A)[2], uint64_t (&B)[2], uint64_t (&R)[2]) {
+            const int s = i % S, t = first_token(i) + tr;
+            if (LOAD == LOAD_TMA && ok) ok = mbar_wait(&sm.full[s], (i / S) & 1);
+            uint64_t a[RUN][2];
+#pragma unroll
+            for (int j = 0; j < RUN; ++j) {
+                uint64_t gv[2], xv[2], u;
+                read(s, t, j, gv, xv);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    gate2(gv[k], a[j][k], u);
+                    const uint64_t b = times_factor2<IN>(in_factor2<IN>(u), xv[k]);
+                    A[k] = j ? f2_mul(A[k], a[j][k]) : a[j][k];
+                    B[k] = j ? f2_fma(a[j][k], B[k], b) : b;
+                }
+            }
+#pragma unroll
+            for (int j = RUN - 1; j >= 0; --j) {
+                uint64_t dv[2];
+                read_d(s, t, j, dv);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) R[k] = f2_mul(a[j][k], j == RUN - 1 ? dv[k] : f2_add(dv[k], R[k]));
+            }
+        };
+        auto hand_on = [&](const uint64_t (&A)[2], const uint64_t (&B)[2], const uint64_t (&R)[2]) {
+            st4(&sm.A[run][ch], A);
+            st4(&sm.B[run][ch], B);
+            st4(&sm.R[run][ch], R);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.sums);
+        };
+        auto finish = [&](int i, uint64_t (&h)[2], uint64_t (&d)[2]) {
+            const int s = i % S, t = first_token(i) + tr;
+            uint64_t a[RUN][2], m[RUN][2], hp[RUN][2];
+#pragma unroll
+            for (int j = 0; j < RUN; ++j) {
+                uint64_t gv[2], xv[2], u;
+                read(s, t, j, gv, xv);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    gate2(gv[k], a[j][k], u);
+                    m[j][k] = in_factor2<IN>(u);
+                    // a h_{t-1} + m' x, dg's factor next to dh
+                    const uint64_t ah = f2_mul(a[j][k], h[k]);
+                    hp[j][k] = slope_fma2<IN>(a[j][k], m[j][k], xv[k], ah);
+                    h[k] = f2_add(times_factor2<IN>(m[j][k], xv[k]), ah);
+                }
+            }
+#pragma unroll
+            for (int j = RUN - 1; j >= 0; --j) {
+                uint64_t dv[2], ox[2], og[2];
+                read_d(s, t, j, dv);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const uint64_t dh = f2_add(dv[k], d[k]);
+                    ox[k] = times_factor2<IN>(m[j][k], dh);
+                    og[k] = f2_mul(hp[j][k], dh);
+                    d[k] = f2_mul(a[j][k], dh);
+                }
+                if (t + j < L) {
+                    put4<LOAD>(xo + (size_t)(t + j) * D, ox, c0 + ch, D);
+                    put4<LOAD>(go + (size_t)(t + j) * D, og, c0 + ch, D);
+                }
+            }
+            if (LOAD == LOAD_TMA) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.empty[s]);
+            }
+        };
+        uint64_t A[2], B[2], R[2], h[2], d[2];
+        for (int i = 0; i <= P.steps; ++i) {
+            if (i < P.steps) compose(i, A, B, R);
+            if (i > 0) {
+                if (ok) ok = mbar_wait(&sm.starts, (i - 1) & 1);
+                ld4(&sm.B[run][ch], h);
+                ld4(&sm.R[run][ch], d);
+            }
+            if (i < P.steps) hand_on(A, B, R);
+            if (i > 0) finish(i - 1, h, d);
+        }
+    } else if (warp == NW) {
+        const bool live = c0 + lane < D;
+        const size_t ns = cdiv(L, kSaveEvery);
+        constexpr int NS = TT / kSaveEvery;   // saved states of a tile
+        float super = P.first && live ? P.first[bh * D + c0 + lane] : 0.f;
+        for (int i = 0; i < P.steps; ++i) {
+            const int t0 = first_token(i);
+            float sv[NS];
 #pragma unroll
             for (int n = 0; n < NS; ++n) {
                 const int t = t0 + n * kSaveEvery;
-                sv[n] = t < L && c0 + tid < D
-                            ? P.saved[(bh * cdiv(L, kSaveEvery) + t / kSaveEvery) * D + c0 + tid] : 0.f;
+                sv[n] = t < L && live ? P.saved[(bh * ns + t / kSaveEvery) * D + c0 + lane] : 0.f;
             }
-        if (LOAD == LOAD_TMA) {
-            if (ok) ok = mbar_wait(&sm.full[s], (i / P.stages) & 1);
-        } else {
-            __syncthreads();   // the previous row's readers
-            fill<CHL, LOAD>(sg, P.g, bh, t0, c0, L, D);
-            fill<CHL, LOAD>(sx, static_cast<const T*>(P.x), bh, t0, c0, L, D);
-            fill<CHL, LOAD>(sd, static_cast<const T*>(P.dO), bh, t0, c0, L, D);
-            __syncthreads();
-        }
-        float a[RUN][VEC], m[RUN][VEC], A[VEC], B[VEC], Q[VEC], R[VEC];
+            if (ok) ok = mbar_wait(&sm.sums, i & 1);
+            float in = super;
+            if (cs > 1) {
+                float tA = 1.f, tR = 0.f;
 #pragma unroll
-        for (int j = 0; j < RUN; ++j) {
-            float gv[VEC], xv[VEC];
-            lds4(sg + (tr + j) * G::CH + ch, gv);
-            lds4(sx + (tr + j) * G::CH + ch, xv);
-#pragma unroll
-            for (int k = 0; k < VEC; ++k) {
-                float u;
-                gate(gv[k], a[j][k], u);
-                m[j][k] = in_factor<IN>(u);
-                A[k] = j ? A[k] * a[j][k] : a[j][k];
-                B[k] = j ? fmaf(a[j][k], B[k], m[j][k] * xv[k]) : m[j][k] * xv[k];
+                for (int r = RUNS - 1; r >= 0; --r) {
+                    const float ra = sm.A[r][lane];
+                    tR = fmaf(ra, tR, sm.R[r][lane]);
+                    tA *= ra;
+                }
+                in = exchange<true>(sm, lane, tA, tR, cs, rank, i, super, ok);
             }
-        }
+            float h = 0.f, d = in;
 #pragma unroll
-        for (int j = RUN - 1; j >= 0; --j) {
-            float dv[VEC];
-            lds4(sd + (tr + j) * G::CH + ch, dv);
-#pragma unroll
-            for (int k = 0; k < VEC; ++k) R[k] = a[j][k] * (j == RUN - 1 ? dv[k] : dv[k] + R[k]);
-        }
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) Q[k] = A[k];
-        warp_compose_up<CHL>(A, B, run);
-        warp_compose_down<CHL>(Q, R, run);
-        if (run == G::RW - 1) {
-            st4(&sm.sum[0][warp][ch], A);
-            st4(&sm.sum[1][warp][ch], B);
-        }
-        if (run == 0) st4(&sm.sum[2][warp][ch], R);
-        float eA[VEC], eB[VEC], fA[VEC], fB[VEC];
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) {
-            eA[k] = __shfl_up_sync(0xffffffffu, A[k], CHL);
-            eB[k] = __shfl_up_sync(0xffffffffu, B[k], CHL);
-            if (run == 0) eA[k] = 1.f, eB[k] = 0.f;
-            fA[k] = __shfl_down_sync(0xffffffffu, Q[k], CHL);
-            fB[k] = __shfl_down_sync(0xffffffffu, R[k], CHL);
-            if (run == G::RW - 1) fA[k] = 1.f, fB[k] = 0.f;
-        }
-        __syncthreads();
-        // every thread is past the previous row, so its stage is free
-        if (LOAD == LOAD_TMA && tid == 0 && i + P.stages - 1 < P.steps) load(i + P.stages - 1);
-        if (tid < G::CH) {
-            float wa[NW], qA[NW], qR[NW], tA = 1.f, tR = 0.f, h = 0.f;
-#pragma unroll
-            for (int w = 0; w < NW; ++w) {
-                wa[w] = sm.sum[0][w][tid];
-                if (w * G::WT % kSaveEvery == 0) h = sv[w * G::WT / kSaveEvery];
-                sm.start[0][w][tid] = h;
-                h = fmaf(wa[w], h, sm.sum[1][w][tid]);
+            for (int r = RUNS - 1; r >= 0; --r) {
+                const float rr = sm.R[r][lane];
+                sm.R[r][lane] = d;
+                d = fmaf(sm.A[r][lane], d, rr);
             }
+            if (cs == 1) super = d;
 #pragma unroll
-            for (int w = NW - 1; w >= 0; --w) {
-                qA[w] = tA, qR[w] = tR;
-                tR = fmaf(wa[w], tR, sm.sum[2][w][tid]);
-                tA *= wa[w];
+            for (int r = 0; r < RUNS; ++r) {
+                if (r * RUN % kSaveEvery == 0) h = sv[r * RUN / kSaveEvery];
+                const float rb = sm.B[r][lane];
+                sm.B[r][lane] = h;
+                h = fmaf(sm.A[r][lane], h, rb);
             }
-            const float in = exchange<CHL, true>(sm, tid, tA, tR, cs, rank, i, super, ok);
-#pragma unroll
-            for (int w = 0; w < NW; ++w) sm.start[1][w][tid] = fmaf(qA[w], in, qR[w]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.starts);
         }
-        __syncthreads();
-        float h[VEC], d[VEC], hp[RUN][VEC];
-        lds4(&sm.start[0][warp][ch], h);
-        lds4(&sm.start[1][warp][ch], d);
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) {
-            h[k] = fmaf(eA[k], h[k], eB[k]);
-            d[k] = fmaf(fA[k], d[k], fB[k]);
-        }
-#pragma unroll
-        for (int j = 0; j < RUN; ++j) {
-            float xv[VEC];
-            lds4(sx + (tr + j) * G::CH + ch, xv);
-#pragma unroll
-            for (int k = 0; k < VEC; ++k) {
-                // a h_{t-1} + m' x, dg's factor next to dh
-                const float ah = a[j][k] * h[k];
-                hp[j][k] = fmaf(in_slope<IN>(a[j][k], m[j][k]), xv[k], ah);
-                h[k] = fmaf(m[j][k], xv[k], ah);
-            }
-        }
-        const size_t at = (bh * L + t0 + tr) * D + c0 + ch;
-        T* xp = static_cast<T*>(P.out) + at;
-        float* gp = P.dg + at;
-#pragma unroll
-        for (int j = RUN - 1; j >= 0; --j) {
-            float dv[VEC];
-            lds4(sd + (tr + j) * G::CH + ch, dv);
-            float ox[VEC], og[VEC];
-#pragma unroll
-            for (int k = 0; k < VEC; ++k) {
-                const float dh = dv[k] + d[k];
-                ox[k] = m[j][k] * dh;
-                og[k] = hp[j][k] * dh;
-                d[k] = a[j][k] * dh;
-            }
-            if (t0 + tr + j < L) {
-                put4<LOAD>(xp + (size_t)j * D, ox, c0 + ch, D);
-                put4<LOAD>(gp + (size_t)j * D, og, c0 + ch, D);
-            }
+        if (P.last && rank == 0 && live) P.last[bh * D + c0 + lane] = super;
+    } else if (LOAD == LOAD_TMA && lane == 0) {
+        for (int i = 0; i < P.steps; ++i) {
+            const int s = i % S, t0 = first_token(i);
+            float* sg = reinterpret_cast<float*>(smem + s * kStage);
+            T* sx = reinterpret_cast<T*>(sg + ELEMS);
+            if (i >= S && ok) ok = mbar_wait(&sm.empty[s], (i / S - 1) & 1);
+            mbar_arrive_expect_tx(&sm.full[s], kStage);
+            tma_load_3d(sg, &mg, c0, t0, (int)bh, &sm.full[s]);
+            tma_load_3d(sx, &mx, c0, t0, (int)bh, &sm.full[s]);
+            tma_load_3d(sx + ELEMS, &md, c0, t0, (int)bh, &sm.full[s]);
         }
     }
-    if (P.last && rank == 0 && tid < G::CH && c0 + tid < D) P.last[bh * D + c0 + tid] = super;
+    __syncwarp();
     if (cs > 1) cluster_sync();
 }
 
@@ -543,9 +613,10 @@ __global__ void __launch_bounds__(NT_D) k_scan_decode(const T* __restrict__ x, c
                                                       float* __restrict__ state, T* __restrict__ o, size_t n) {
     const size_t i = (size_t)blockIdx.x * NT_D + threadIdx.x;
     if (i >= n) return;
-    float a, u;
-    gate(g[i], a, u);
-    const float h = fmaf(a, state[i], in_factor<IN>(u) * to_f(x[i]));
+    uint64_t a, t;
+    gate2(f2_all(g[i]), a, t);
+    float h, unused;
+    f2_split(f2_fma(a, f2_all(state[i]), times_factor2<IN>(in_factor2<IN>(t), f2_all(to_f(x[i])))), h, unused);
     state[i] = h;
     o[i] = from_f<T>(h);
 }
@@ -576,59 +647,87 @@ gla_status check(const gla_problem* p) {
 }
 bool input_ok(int input) { return input >= GLA_SCAN_PLAIN && input <= GLA_SCAN_NORM; }
 
-// 3D map over [BH][L][D] with a box of box_l x box_c.
+// 3D map over [BH][L][D] with a box of TT tokens x CH channels.
 template <typename T>
-bool scan_map(CUtensorMap* m, const void* base, int D, int L, int BH, int box_c, int box_l) {
+bool scan_map(CUtensorMap* m, const void* base, int D, int L, int BH) {
     auto fn = tc::encode_fn();
     if (!fn) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)L, (cuuint64_t)BH};
     const cuuint64_t strides[2] = {(cuuint64_t)D * sizeof(T), (cuuint64_t)D * sizeof(T) * L};
-    const cuuint32_t box[3] = {(cuuint32_t)box_c, (cuuint32_t)box_l, 1}, estr[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {CH, TT, 1}, estr[3] = {1, 1, 1};
     return fn(m, std::is_same<T, float>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
               const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Launches a walk: chooses the channels of a tile, the cluster and the ring.
-template <typename T, int IN, int CHL, int LOAD, bool BWD>
+// CTAs that the current device holds at once in clusters of `cs`, asked of the runtime once per kernel and
+// device (a cluster stays within a GPC, so not every SM is filled by every size).
+template <typename K>
+int resident_ctas(K kern, cudaLaunchConfig_t cfg, int cs, size_t smem, std::atomic<int> (&known)[kMaxCluster + 1]) {
+    int n = known[cs].load(std::memory_order_relaxed);
+    if (n) return n;
+    cfg.attrs[0].val.clusterDim.x = cs;
+    cfg.gridDim = dim3(cs);
+    cfg.dynamicSmemBytes = smem;
+    int clusters = 0;
+    if (cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        clusters = 0;
+    }
+    n = clusters > 0 ? clusters * cs : -1;
+    known[cs].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+// Launches a walk. CTAs per cluster: the split with the least time in a model of equal waves, each as many rows of
+// tiles as a CTA walks plus kFill for filling and draining its pipeline. Measured (forward, us): 256
+// chains of 16 tiles 26 / 36 / 43 / 56 in clusters of 1 / 2 / 4 / 8; 32 chains of 512 tiles 387 / 291 /
+// 149 / 99.
+template <typename T, int IN, int LOAD, bool BWD>
 cudaError_t launch_walk(const gla_problem* p, ScanArgs P, const CUtensorMap (&maps)[3], cudaStream_t st) {
-    using G = Geo<CHL>;
-    P.nblk = cdiv(P.D, G::CH);
+    constexpr int kFill = 4;
+    P.nblk = cdiv(P.D, CH);
     const long long chains = (long long)p->B * p->H * P.nblk;
-    const int tiles = cdiv(P.L, G::TT), want = tc::num_sms() * 3;
-    int cs = 1;
-    while (cs < kMaxCluster && chains * cs < want && cs < tiles) cs *= 2;
-    P.steps = cdiv(tiles, cs);
-    constexpr int kStage = G::ELEMS * (4 + (BWD ? 2 : 1) * (int)sizeof(T));
-    constexpr int most = LOAD == LOAD_TMA ? (BWD ? 3 : sizeof(T) == 2 ? 3 : 2) : 1;
-    P.stages = P.steps < most ? P.steps : most;
-    if (BWD && LOAD == LOAD_TMA && P.stages < 2) P.stages = 2;
-    if (P.stages < 1) P.stages = 1;
-    const size_t bytes = (size_t)P.stages * kStage + sizeof(Tail<CHL, BWD ? 3 : 2>);
+    const int tiles = cdiv(P.L, TT);
+    constexpr int kStage = ELEMS * (4 + (BWD ? 2 : 1) * (int)sizeof(T));
+    constexpr size_t ring = LOAD == LOAD_TMA ? (size_t)kStage * (BWD ? bwd_stages<T>() : kFwdStages) : 0;
+    constexpr size_t tail = BWD ? sizeof(BwdTail<bwd_stages<T>()>) : sizeof(FwdTail);
+    auto smem = [&](int c) { return ring + tail + (c > 1 ? 2 * CH * sizeof(float2) * c : 0); };
+    auto kern = [] {
+        if constexpr (BWD) return k_scan_bwd<T, IN, LOAD>;
+        else return k_scan_fwd<T, IN, LOAD>;
+    }();
     static std::atomic<bool> seen[kMaxDevices];
-    const size_t top = (size_t)(most < 2 ? 2 : most) * kStage + sizeof(Tail<CHL, BWD ? 3 : 2>);
-    cudaError_t e;
+    static std::atomic<int> known[kMaxDevices][kMaxCluster + 1];
+    cudaError_t e = smem_attr_once(kern, smem(kMaxCluster), seen);
+    if (e != cudaSuccess) return e;
+    int dev = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(chains * cs));
-    cfg.blockDim = dim3(NT_S);
-    cfg.dynamicSmemBytes = bytes;
+    cfg.blockDim = dim3(NT_F);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = cs;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[0].val.clusterDim.x = attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if constexpr (BWD) {
-        auto kern = k_scan_bwd<T, IN, CHL, LOAD>;
-        if ((e = smem_attr_once(kern, top, seen)) != cudaSuccess) return e;
-        GLA_LAUNCH("scan_bwd", st, (e = cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], maps[2], P, cs)));
-    } else {
-        auto kern = k_scan_fwd<T, IN, CHL, LOAD>;
-        if ((e = smem_attr_once(kern, top, seen)) != cudaSuccess) return e;
-        GLA_LAUNCH("scan_fwd", st, (e = cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], P, cs)));
+    int cs = 1;
+    long long best = -1;
+    for (int c = 1; c <= kMaxCluster && (c == 1 || c <= tiles); ++c) {
+        const int slots = resident_ctas(kern, cfg, c, smem(c), known[dev]);
+        if (slots <= 0) continue;
+        const long long cost = (chains * c + slots - 1) / slots * (cdiv(tiles, c) + kFill);
+        if (best < 0 || cost < best) best = cost, cs = c;
     }
+    P.steps = cdiv(tiles, cs);
+    attr[0].val.clusterDim.x = cs;
+    cfg.gridDim = dim3((unsigned)(chains * cs));
+    cfg.dynamicSmemBytes = smem(cs);
+    if constexpr (BWD)
+        GLA_LAUNCH("scan_bwd", st, (e = cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], maps[2], P, cs)));
+    else
+        GLA_LAUNCH("scan_fwd", st, (e = cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], P, cs)));
     return e;
 }
 
@@ -637,21 +736,16 @@ cudaError_t walk(const gla_problem* p, const ScanArgs& P, cudaStream_t st) {
     CUtensorMap maps[3] = {};
     const int BH = p->B * p->H, D = P.D, L = P.L;
     // TMA boxes need rows of whole 16-byte pieces, and are not used for rows shorter than a box
-    if (D % (16 / (int)sizeof(T)) == 0 && D >= 32 && L > 0) {
-        const bool wide = D >= 64 && (long long)BH * cdiv(D, 64) * kMaxCluster >= 3 * tc::num_sms();
-        const int ch = wide ? Geo<16>::CH : Geo<8>::CH, tt = wide ? Geo<16>::TT : Geo<8>::TT;
-        if (scan_map<T>(&maps[0], P.x, D, L, BH, ch, tt) && scan_map<float>(&maps[1], P.g, D, L, BH, ch, tt) &&
-            (!BWD || scan_map<T>(&maps[2], P.dO, D, L, BH, ch, tt)))
-            return wide ? launch_walk<T, IN, 16, LOAD_TMA, BWD>(p, P, maps, st)
-                        : launch_walk<T, IN, 8, LOAD_TMA, BWD>(p, P, maps, st);
-    }
-    return D % 4 == 0 ? launch_walk<T, IN, 8, LOAD_VEC4, BWD>(p, P, maps, st)
-                      : launch_walk<T, IN, 8, LOAD_ONE, BWD>(p, P, maps, st);
+    if (D % (16 / (int)sizeof(T)) == 0 && D >= CH && L > 0 && scan_map<T>(&maps[0], P.x, D, L, BH) &&
+        scan_map<float>(&maps[1], P.g, D, L, BH) && (!BWD || scan_map<T>(&maps[2], P.dO, D, L, BH)))
+        return launch_walk<T, IN, LOAD_TMA, BWD>(p, P, maps, st);
+    return D % 4 == 0 ? launch_walk<T, IN, LOAD_VEC4, BWD>(p, P, maps, st)
+                      : launch_walk<T, IN, LOAD_ONE, BWD>(p, P, maps, st);
 }
 
 cudaError_t fwd(const gla_problem* p, int input, const void* x, const float* g, const float* h0, void* o, float* hT,
                 float* saved, cudaStream_t st) {
-    const ScanArgs P{x, g, nullptr, h0, o, nullptr, hT, saved, p->L, p->Dk, 0, 0, 0};
+    const ScanArgs P{x, g, nullptr, h0, o, nullptr, hT, saved, p->L, p->Dk, 0, 0};
     return dispatch(p, input, [&](auto tv, auto in) {
         return walk<decltype(tv), decltype(in)::value, false>(p, P, st);
     });
@@ -720,7 +814,7 @@ gla_status gla_scan_bwd_saved(const gla_problem* p, int input, const void* x, co
         if (e != cudaSuccess) return record_cuda(e, "scan states");
         saved = own;
     }
-    const ScanArgs P{x, g, dO, dhT, dx, dg, dh0, const_cast<float*>(saved), p->L, p->Dk, 0, 0, 0};
+    const ScanArgs P{x, g, dO, dhT, dx, dg, dh0, const_cast<float*>(saved), p->L, p->Dk, 0, 0};
     const cudaError_t e = dispatch(p, input, [&](auto tv, auto in) {
         return walk<decltype(tv), decltype(in)::value, true>(p, P, st);
     });
