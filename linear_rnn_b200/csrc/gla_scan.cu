@@ -89,30 +89,30 @@ __device__ __forceinline__ void gate2(uint64_t g, uint64_t& a, uint64_t& t) {
     t = f2(n0 ? t0 : q0, n1 ? t1 : q1);
 }
 
-// The factor on the input, from t. u = 1 - a^2 = t (2 - t); u < 0 (g > 0) gives NaN like the formula,
-// u below the normal numbers 0.
+// The factor on the input, from t, and for GLA_SCAN_NORM its inverse (0 where the factor is 0).
+// u = 1 - a^2 = t (2 - t), m = u / sqrt(u); u < 0 (g > 0) gives NaN like the formula, u below the normal
+// numbers 0.
 template <int IN>
-__device__ __forceinline__ uint64_t in_factor2(uint64_t t) {
+__device__ __forceinline__ uint64_t in_factor2(uint64_t t, uint64_t& inv) {
     if (IN == GLA_SCAN_PLAIN) return f2_all(1.f);
     if (IN == GLA_SCAN_COMPLEMENT) return t;
+    const uint64_t u = f2_mul(t, f2_fma(t, f2_all(-1.f), f2_all(2.f)));
     float u0, u1;
-    f2_split(f2_mul(t, f2_fma(t, f2_all(-1.f), f2_all(2.f))), u0, u1);
-    const float m0 = u0 * rsqrt_approx(u0), m1 = u1 * rsqrt_approx(u1);
-    return f2(fabsf(u0) < 1.1754944e-38f ? 0.f : m0, fabsf(u1) < 1.1754944e-38f ? 0.f : m1);
+    f2_split(u, u0, u1);
+    inv = f2(fabsf(u0) < 1.1754944e-38f ? 0.f : rsqrt_approx(u0),
+             fabsf(u1) < 1.1754944e-38f ? 0.f : rsqrt_approx(u1));
+    return f2_mul(u, inv);
 }
 template <int IN>
 __device__ __forceinline__ uint64_t times_factor2(uint64_t m, uint64_t x) {
     return IN == GLA_SCAN_PLAIN ? x : f2_mul(m, x);
 }
-// Its derivative with respect to g times x, plus c.
+// The factor's derivative with respect to g (0, -a, -a^2 / m) times x, plus c.
 template <int IN>
-__device__ __forceinline__ uint64_t slope_fma2(uint64_t a, uint64_t m, uint64_t x, uint64_t c) {
+__device__ __forceinline__ uint64_t slope_fma2(uint64_t a, uint64_t inv, uint64_t x, uint64_t c) {
     if (IN == GLA_SCAN_PLAIN) return c;
-    if (IN == GLA_SCAN_COMPLEMENT) return f2_fma(f2_mul(a, f2_all(-1.f)), x, c);
-    float m0, m1;
-    f2_split(m, m0, m1);
-    const float r0 = m0 == 0.f ? 0.f : -tc::rcp_approx(m0), r1 = m1 == 0.f ? 0.f : -tc::rcp_approx(m1);
-    return f2_fma(f2_mul(f2_mul(a, a), f2(r0, r1)), x, c);
+    const uint64_t ax = f2_mul(f2_mul(a, f2_all(-1.f)), x);
+    return IN == GLA_SCAN_COMPLEMENT ? f2_add(ax, c) : f2_fma(f2_mul(a, inv), ax, c);
 }
 
 // ------------------------------------------------------------------ four channels of a token
@@ -297,9 +297,9 @@ __global__ void __launch_bounds__(NT_F, 2)
             for (int j = 0; j < RUN; ++j)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    uint64_t u;
+                    uint64_t u, inv;
                     gate2(gv[j][k], a[j][k], u);
-                    b[j][k] = times_factor2<IN>(in_factor2<IN>(u), xv[j][k]);
+                    b[j][k] = times_factor2<IN>(in_factor2<IN>(u, inv), xv[j][k]);
                     A[k] = j ? f2_mul(A[k], a[j][k]) : a[j][k];
                     B[k] = j ? f2_fma(a[j][k], B[k], b[j][k]) : b[j][k];
                 }
@@ -472,12 +472,12 @@ __global__ void __launch_bounds__(NT_F, 2)
             uint64_t a[RUN][2];
 #pragma unroll
             for (int j = 0; j < RUN; ++j) {
-                uint64_t gv[2], xv[2], u;
+                uint64_t gv[2], xv[2], u, inv;
                 read(s, t, j, gv, xv);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     gate2(gv[k], a[j][k], u);
-                    const uint64_t b = times_factor2<IN>(in_factor2<IN>(u), xv[k]);
+                    const uint64_t b = times_factor2<IN>(in_factor2<IN>(u, inv), xv[k]);
                     A[k] = j ? f2_mul(A[k], a[j][k]) : a[j][k];
                     B[k] = j ? f2_fma(a[j][k], B[k], b) : b;
                 }
@@ -502,15 +502,15 @@ __global__ void __launch_bounds__(NT_F, 2)
             uint64_t a[RUN][2], m[RUN][2], hp[RUN][2];
 #pragma unroll
             for (int j = 0; j < RUN; ++j) {
-                uint64_t gv[2], xv[2], u;
+                uint64_t gv[2], xv[2], u, inv;
                 read(s, t, j, gv, xv);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     gate2(gv[k], a[j][k], u);
-                    m[j][k] = in_factor2<IN>(u);
+                    m[j][k] = in_factor2<IN>(u, inv);
                     // a h_{t-1} + m' x, dg's factor next to dh
                     const uint64_t ah = f2_mul(a[j][k], h[k]);
-                    hp[j][k] = slope_fma2<IN>(a[j][k], m[j][k], xv[k], ah);
+                    hp[j][k] = slope_fma2<IN>(a[j][k], inv, xv[k], ah);
                     h[k] = f2_add(times_factor2<IN>(m[j][k], xv[k]), ah);
                 }
             }
@@ -613,10 +613,10 @@ __global__ void __launch_bounds__(NT_D) k_scan_decode(const T* __restrict__ x, c
                                                       float* __restrict__ state, T* __restrict__ o, size_t n) {
     const size_t i = (size_t)blockIdx.x * NT_D + threadIdx.x;
     if (i >= n) return;
-    uint64_t a, t;
+    uint64_t a, t, inv;
     gate2(f2_all(g[i]), a, t);
     float h, unused;
-    f2_split(f2_fma(a, f2_all(state[i]), times_factor2<IN>(in_factor2<IN>(t), f2_all(to_f(x[i])))), h, unused);
+    f2_split(f2_fma(a, f2_all(state[i]), times_factor2<IN>(in_factor2<IN>(t, inv), f2_all(to_f(x[i])))), h, unused);
     state[i] = h;
     o[i] = from_f<T>(h);
 }
