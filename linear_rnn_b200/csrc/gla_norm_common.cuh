@@ -1,0 +1,470 @@
+// What the norms around a block share (gla_addnorm.cu, gla_headnorm.cu):
+//   norm(r) = n = (r - mu) rstd,  rstd = 1 / sqrt(mean((r - mu)^2) + eps);  mu = 0 for the RMS norm.
+// Gradient of a norm, d the gradient of n:  dr = rstd (d - n mean(d n) - [layer] mean(d)); with
+// mean(d n) = rstd mean(d (r - mu)) it needs one set of row sums for the RMS norm and two for the layer
+// norm (mu, then the sums about it).
+//
+// The kernels are bound by HBM, and next by instruction issue (a bf16 element has 10 to 14 bytes of
+// traffic to hide about 30 instructions behind). So a row is read once and held by the G threads that
+// share it, 16 elements a thread where the row is long, so that the row sums' exchange is spread over
+// many elements; arithmetic is on packed pairs of fp32; several sums share their shuffles; and
+// every thread copies its own pieces of the next rows into shared memory asynchronously (a ring that only
+// its own thread reads, so no barrier guards it). Rows of up to 512 elements belong to a warp or
+// less, longer ones to a block. Blocks walk many rows and keep the column sums (dw) in registers.
+#pragma once
+#include <type_traits>
+
+#include "gla_common.cuh"
+#include "gla_plans.h"
+#include "gla_tc_common.cuh"
+#include "sm100.cuh"
+
+namespace gla {
+namespace norm {
+
+using namespace sm100;
+using tc::f2;
+using tc::f2_fma;
+using tc::f2_mul;
+
+// ------------------------------------------------------------------ packed pairs of fp32
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ void f2_split(uint64_t v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t f2_all(float v) { return f2(v, v); }
+__device__ __forceinline__ float f2_sum(uint64_t v) {
+    float a, b;
+    f2_split(v, a, b);
+    return a + b;
+}
+
+// ------------------------------------------------------------------ pieces of a row
+// A piece: VEC elements, held as NP pairs (VEC = 1: one pair whose second half is 0).
+template <int VEC>
+constexpr int kPairs = VEC == 1 ? 1 : VEC / 2;
+
+template <int VEC>
+__device__ __forceinline__ void load_piece(const float* p, uint64_t (&v)[kPairs<VEC>]) {
+    if constexpr (VEC == 1) {
+        v[0] = f2(*p, 0.f);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC / 4; ++i) {
+            const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(p + 4 * i);
+            v[2 * i] = u.x;
+            v[2 * i + 1] = u.y;
+        }
+    }
+}
+template <int VEC>
+__device__ __forceinline__ void load_piece(const __nv_bfloat16* p, uint64_t (&v)[kPairs<VEC>]) {
+    if constexpr (VEC == 1) {
+        v[0] = f2(__bfloat162float(*p), 0.f);
+    } else {
+        uint32_t w[VEC / 2];
+        if constexpr (VEC == 8) {
+            const uint4 u = *reinterpret_cast<const uint4*>(p);
+            w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+        } else {
+            const uint2 u = *reinterpret_cast<const uint2*>(p);
+            w[0] = u.x; w[1] = u.y;
+        }
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) v[i] = f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    }
+}
+template <int VEC>
+__device__ __forceinline__ void store_piece(float* p, const uint64_t (&v)[kPairs<VEC>]) {
+    if constexpr (VEC == 1) {
+        float a, b;
+        f2_split(v[0], a, b);
+        *p = a;
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC / 4; ++i)
+            *reinterpret_cast<ulonglong2*>(p + 4 * i) = make_ulonglong2(v[2 * i], v[2 * i + 1]);
+    }
+}
+__device__ __forceinline__ uint32_t to_bf16x2(uint64_t v) {
+    float a, b;
+    f2_split(v, a, b);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <int VEC>
+__device__ __forceinline__ void store_piece(__nv_bfloat16* p, const uint64_t (&v)[kPairs<VEC>]) {
+    if constexpr (VEC == 1) {
+        float a, b;
+        f2_split(v[0], a, b);
+        *p = __float2bfloat16_rn(a);
+    } else if constexpr (VEC == 8) {
+        *reinterpret_cast<uint4*>(p) =
+            make_uint4(to_bf16x2(v[0]), to_bf16x2(v[1]), to_bf16x2(v[2]), to_bf16x2(v[3]));
+    } else {
+        *reinterpret_cast<uint2*>(p) = make_uint2(to_bf16x2(v[0]), to_bf16x2(v[1]));
+    }
+}
+
+// Where a thread's pieces of a row are.
+struct Place {
+    int at, G, nvec;
+    __device__ __forceinline__ bool has(int j) const { return at + j * G < nvec; }
+    template <int VEC>
+    __device__ __forceinline__ int col(int j) const { return (at + j * G) * VEC; }
+};
+
+// ------------------------------------------------------------------ the ring
+// S stages of shared memory that belong to the thread alone: piece j of input `in` of a stage lies, in units of
+// 16 bytes (8 for bf16 pieces of four), blockDim units apart from the next, so a warp's accesses
+// are contiguous. Stages are written by cp.async, one commit group per row; wait() leaves the groups of
+// the S - 1 rows that follow in flight.
+template <int S>
+struct Feed {
+    uint8_t* mine;      // this thread's first byte, in the first stage
+    int stage_bytes, unit_stride;
+    int s;              // stage of the current row
+
+    // Room of one input's NV pieces, in bytes per thread.
+    template <typename T, int VEC, int NV>
+    static constexpr int bytes() { return VEC * (int)sizeof(T) * NV; }
+
+    template <typename T, int VEC>
+    __device__ __forceinline__ uint8_t* at(int stage, int thread_off, int j) const {
+        constexpr int B = VEC * (int)sizeof(T);
+        return mine + stage * stage_bytes + (thread_off + j * B) * (int)blockDim.x;
+    }
+    template <typename T, int VEC>
+    __device__ __forceinline__ void copy(int stage, int thread_off, int j, const T* src) const {
+        constexpr int B = VEC * (int)sizeof(T);
+        uint8_t* d = at<T, VEC>(stage, thread_off, j);
+        if constexpr (B >= 16) {
+#pragma unroll
+            for (int u = 0; u < B / 16; ++u)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(d + u * 16 * (int)blockDim.x)),
+                             "l"(reinterpret_cast<const uint8_t*>(src) + 16 * u)
+                             : "memory");
+        } else {
+            // threads of 8-byte pieces share 16-byte units
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(d - 8 * (int)threadIdx.x)), "l"(src)
+                         : "memory");
+        }
+    }
+    template <typename T, int VEC>
+    __device__ __forceinline__ void read(int thread_off, int j, uint64_t (&v)[kPairs<VEC>]) const {
+        constexpr int B = VEC * (int)sizeof(T);
+        const uint8_t* d = at<T, VEC>(s, thread_off, j);
+        if constexpr (B == 32) {   // eight fp32: two units
+            uint64_t a[2], b[2];
+            load_piece<4>(reinterpret_cast<const float*>(d), a);
+            load_piece<4>(reinterpret_cast<const float*>(d + 16 * (int)blockDim.x), b);
+            v[0] = a[0]; v[1] = a[1]; v[2] = b[0]; v[3] = b[1];
+        } else if constexpr (B == 16) {
+            load_piece<VEC>(reinterpret_cast<const T*>(d), v);
+        } else {
+            load_piece<VEC>(reinterpret_cast<const T*>(d - 8 * (int)threadIdx.x), v);
+        }
+    }
+    __device__ __forceinline__ void commit() const { asm volatile("cp.async.commit_group;" ::: "memory"); }
+    __device__ __forceinline__ void wait() const {
+        asm volatile("cp.async.wait_group %0;" ::"n"(S > 2 ? S - 2 : 0) : "memory");
+    }
+    __device__ __forceinline__ int ahead() const { return s == 0 ? S - 1 : s - 1; }   // stage of the row S - 1 ahead
+    __device__ __forceinline__ void next() { s = s + 1 == S ? 0 : s + 1; }
+};
+
+// ------------------------------------------------------------------ sums over a row
+// Sums of K <= 4 values over the G threads of a row; every thread of the block calls. G < 32: plain
+// shuffles (G a power of two). From a warp up, K values share their shuffles: each exchange halves either the
+// lanes or the values a lane still carries. G > 32: the block is one row; a warp's sums go through
+// `buf`, which alternates between two halves so that one barrier per call is enough.
+struct RowSum {
+    float* buf;   // [2][32 warps][4]
+    int G, half;
+
+    template <int K>
+    __device__ __forceinline__ void operator()(float (&v)[K]) {
+        static_assert(K >= 1 && K <= 4, "");
+        const int lane = threadIdx.x & 31;
+        if (G < 32) {
+            for (int off = G >> 1; off; off >>= 1)
+#pragma unroll
+                for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], off);
+            return;
+        }
+        // after this, lanes of index 32 / KP * k .. hold the warp's sum k in x
+        constexpr int KP = K == 1 ? 1 : K == 2 ? 2 : 4;
+        float x;
+        if constexpr (KP == 1) {
+            x = v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
+            x += __shfl_xor_sync(0xffffffffu, x, 8);
+        } else if constexpr (KP == 2) {
+            const bool hi = lane & 16;
+            x = (hi ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, hi ? v[0] : v[1], 16);
+            x += __shfl_xor_sync(0xffffffffu, x, 8);
+        } else {
+            const float v3 = K == 4 ? v[K - 1] : 0.f;
+            const bool hi = lane & 16, mid = lane & 8;
+            const float a = (hi ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, hi ? v[0] : v[2], 16);
+            const float b = (hi ? v3 : v[1]) + __shfl_xor_sync(0xffffffffu, hi ? v[1] : v3, 16);
+            x = (mid ? b : a) + __shfl_xor_sync(0xffffffffu, mid ? a : b, 8);
+        }
+        x += __shfl_xor_sync(0xffffffffu, x, 4);
+        x += __shfl_xor_sync(0xffffffffu, x, 2);
+        x += __shfl_xor_sync(0xffffffffu, x, 1);
+        constexpr int W = 32 / KP;
+        if (G == 32) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) v[k] = __shfl_sync(0xffffffffu, x, W * k);
+            return;
+        }
+        float* b = buf + half * 128;
+        half ^= 1;
+        const int warp = threadIdx.x >> 5, nw = G >> 5;
+        if ((lane & (W - 1)) == 0) b[warp * 4 + lane / W] = x;
+        __syncthreads();
+        // lane = 4 warp + k: adds the warps 8 apart, then over the lanes of one k
+        x = 0.f;
+        for (int w = lane >> 2; w < nw; w += 8)
+            if ((lane & 3) < K) x += b[w * 4 + (lane & 3)];
+        x += __shfl_xor_sync(0xffffffffu, x, 4);
+        x += __shfl_xor_sync(0xffffffffu, x, 8);
+        x += __shfl_xor_sync(0xffffffffu, x, 16);
+#pragma unroll
+        for (int k = 0; k < K; ++k) v[k] = __shfl_sync(0xffffffffu, x, k);
+    }
+};
+
+// r -= mean(r) for the layer norm (elements beyond the row stay 0).
+template <int KIND, int VEC, int NV>
+__device__ __forceinline__ void center(RowSum& sum, uint64_t (&r)[NV][kPairs<VEC>], const Place& P, float inv_d) {
+    if (KIND != GLA_NORM_LAYER) return;
+    uint64_t t = 0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < kPairs<VEC>; ++i) t = f2_add(t, r[j][i]);
+    float s[1] = {f2_sum(t)};
+    sum(s);
+    const float mu = -s[0] * inv_d;
+    const uint64_t m2 = VEC == 1 ? f2(mu, 0.f) : f2_all(mu);
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+        if (P.has(j))
+#pragma unroll
+            for (int i = 0; i < kPairs<VEC>; ++i) r[j][i] = f2_add(r[j][i], m2);
+}
+
+template <int VEC, int NV>
+__device__ __forceinline__ float square_sum(const uint64_t (&r)[NV][kPairs<VEC>]) {
+    uint64_t t = 0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < kPairs<VEC>; ++i) t = f2_fma(r[j][i], r[j][i], t);
+    return f2_sum(t);
+}
+
+// This thread's columns of a weight vector times c (null: c).
+template <int VEC, int NV>
+__device__ __forceinline__ void load_columns(uint64_t (&v)[NV][kPairs<VEC>], const float* p, const Place& P, float c) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+#pragma unroll
+        for (int i = 0; i < kPairs<VEC>; ++i) v[j][i] = f2_all(1.f);
+        if (p && P.has(j)) load_piece<VEC>(p + P.col<VEC>(j), v[j]);
+#pragma unroll
+        for (int i = 0; i < kPairs<VEC>; ++i) v[j][i] = f2_mul(v[j][i], f2_all(c));
+    }
+}
+
+// Sums a column accumulator over the row groups of a block and writes the block's partial row.
+// smem: blockDim * NV * VEC floats where the block has several rows.
+template <int VEC, int NV>
+__device__ __forceinline__ void write_partial(const uint64_t (&acc)[NV][kPairs<VEC>], float* smem, int grp,
+                                              const Place& P, float* out) {
+    const int D = P.nvec * VEC, ngrp = P.G >= 32 && P.G == (int)blockDim.x ? 1 : blockDim.x / P.G;
+    if (ngrp == 1) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (P.has(j)) store_piece<VEC>(out + P.col<VEC>(j), acc[j]);
+        return;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+        if (P.has(j))
+#pragma unroll
+            for (int i = 0; i < kPairs<VEC>; ++i) {
+                float a, b;
+                f2_split(acc[j][i], a, b);
+                smem[grp * D + P.col<VEC>(j) + 2 * i] = a;
+                if (VEC > 1) smem[grp * D + P.col<VEC>(j) + 2 * i + 1] = b;
+            }
+    __syncthreads();
+    for (int c = threadIdx.x; c < D; c += blockDim.x) {
+        float s = 0.f;
+        for (int k = 0; k < ngrp; ++k) s += smem[k * D + c];
+        out[c] = s;
+    }
+}
+
+// ------------------------------------------------------------------ partial rows -> dw
+// out[c] = sum over i < n of part[i * stride + c]: 32 columns per block, 32 rows at a time. blockIdx.y
+// picks one of two sums.
+static __global__ void __launch_bounds__(1024) k_colsum(const float* __restrict__ part0, float* __restrict__ out0,
+                                                        const float* __restrict__ part1, float* __restrict__ out1,
+                                                        int n, size_t stride, int cols) {
+    __shared__ float red[32][33];
+    const float* part = blockIdx.y ? part1 : part0;
+    float* out = blockIdx.y ? out1 : out0;
+    grid_dep_wait();   // launched while the kernel that writes the partial rows drains
+    const int c = blockIdx.x * 32 + threadIdx.x;
+    float s = 0.f;
+    if (c < cols)
+#pragma unroll 8
+        for (int i = threadIdx.y; i < n; i += 32) s += part[(size_t)i * stride + c];
+    red[threadIdx.y][threadIdx.x] = s;
+    __syncthreads();
+    s = red[threadIdx.x][threadIdx.y];
+#pragma unroll
+    for (int off = 16; off; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    const int cc = blockIdx.x * 32 + threadIdx.y;
+    if (threadIdx.x == 0 && cc < cols) out[cc] = s;
+}
+// One or two column sums (out1 may be null).
+inline cudaError_t colsum(const float* part0, float* out0, const float* part1, float* out1, int n, size_t stride,
+                          int cols, cudaStream_t st) {
+    if (!out0) {
+        part0 = part1, out0 = out1;
+        out1 = nullptr;
+    }
+    if (!out0) return cudaSuccess;
+    cudaError_t e;
+    GLA_LAUNCH("norm_colsum", st,
+               (e = tc::launch_ex(k_colsum, dim3(cdiv(cols, 32), out1 ? 2 : 1), dim3(32, 32), 0, st, n > 0, 1, part0,
+                                      out0, part1, out1, n, stride, cols)));
+    return e;
+}
+
+// ------------------------------------------------------------------ host side
+// Threads and pieces of a row. A piece is 16 bytes of the widest type in the row (8 bf16, or 4 where
+// fp32 stands beside them: with 8 the fp32 accesses of a warp would leave every other 16 bytes out,
+// 305 instead of 224 us for the backward of 16384 x 4096 with an fp32 residual), 4 elements where D is
+// no multiple of 8, one where it is odd. One piece a thread while a warp's lanes hold the row,
+// 16 elements a thread beyond (4 for single elements up to D = 2048); a power of two of lanes up to a
+// warp (D <= 512), whole warps beyond.
+struct RowPlan {
+    int vec, nv, G, threads;
+    bool big;   // more than 512 threads: D > 8192
+};
+inline RowPlan row_plan(int D, bool all_bf16) {
+    RowPlan p;
+    p.vec = all_bf16 && D % 8 == 0 ? 8 : D % 4 == 0 ? 4 : 1;
+    const int nvec = D / p.vec;
+    p.nv = nvec <= 32 ? 1 : p.vec == 1 && D <= 2048 ? 4 : 16 / p.vec;
+    const int need = cdiv(nvec, p.nv);
+    if (need > 32) {
+        p.G = cdiv(need, 32) * 32;
+        p.threads = p.G;
+    } else {
+        for (p.G = 1; p.G < need;) p.G *= 2;
+        p.threads = 256;
+    }
+    p.big = p.threads > 512;
+    return p;
+}
+// Shared memory in front of the ring: the row sums' buffer; it and the ring are free again when the column
+// sums of a block's row groups need their blockDim * 16 floats at most.
+constexpr int kHead = 1024;
+constexpr int kSmSmem = 220 * 1024;    // of an SM, for its blocks
+// Stages of the ring: 3 where two blocks of them fit an SM, else 2 where one does, else none (as for pieces of
+// one element).
+inline int ring_stages(const RowPlan& p, int thread_bytes) {
+    const int row = thread_bytes * p.threads;
+    if (p.vec == 1 || p.big) return 0;
+    if (2 * (3 * row + kHead + 1024) <= kSmSmem) return 3;
+    return p.nv > 1 && 2 * row + kHead + 1024 <= kSmSmem ? 2 : 0;
+}
+inline size_t block_smem(const RowPlan& p, int stages, int thread_bytes) {
+    const size_t ring = kHead + (size_t)stages * thread_bytes * p.threads;
+    const size_t cols = p.threads == p.G ? 0 : (size_t)4 * p.threads * p.nv * p.vec;
+    return ring > cols ? ring : cols;
+}
+
+// Blocks that walk the rows, and so partial rows of the column sums: no more than give every SM
+// 1024 threads, 2048 where a warp holds a row. The launch takes fewer where fewer fit, so that no block
+// waits for another.
+inline int row_blocks(const RowPlan& p, long long rows, int heads) {
+    const int per = p.threads / p.G;
+    const long long need = (rows + per - 1) / per;
+    long long most = (long long)tc::num_sms() * ((p.G <= 32 ? 2048 : 1024) / p.threads) / heads;
+    if (most < 1) most = 1;
+    return (int)(need < most ? need : most);
+}
+template <typename K>
+int fit_blocks(K kern, const RowPlan& p, size_t smem, int blocks, int heads) {
+    if ((long long)blocks * heads <= tc::num_sms()) return blocks;
+    int per_sm = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, p.threads, smem) != cudaSuccess || per_sm < 1) {
+        cudaGetLastError();
+        return blocks;
+    }
+    const int fit = tc::num_sms() * per_sm / heads;
+    return fit < 1 ? 1 : fit < blocks ? fit : blocks;
+}
+
+// Picks the kernel's shape: VEC, NV, ring stages, largest block.
+template <int V, int N, int S, int M> struct Shape {
+    static constexpr int vec = V, nv = N, stages = S, maxt = M;
+};
+// BF16: every operand of the row is bf16, so pieces of 8 exist too.
+template <bool BF16, typename F>
+cudaError_t by_shape(const RowPlan& p, int stages, F&& f) {
+    constexpr int W = BF16 ? 8 : 4;
+    if (p.vec == 1) {
+        if (p.big) return f(Shape<1, 16, 0, 1024>{});
+        if (p.nv == 1) return f(Shape<1, 1, 0, 512>{});
+        return p.nv == 4 ? f(Shape<1, 4, 0, 512>{}) : f(Shape<1, 16, 0, 512>{});
+    }
+    if (p.vec == W) {
+        if (p.nv == 1) return f(Shape<W, 1, 3, 512>{});
+        if (stages == 0) return f(Shape<W, 16 / W, 0, 1024>{});
+        return stages == 3 ? f(Shape<W, 16 / W, 3, 512>{}) : f(Shape<W, 16 / W, 2, 512>{});
+    }
+    if constexpr (W == 8) {   // D a multiple of 4 only
+        if (p.nv == 1) return f(Shape<4, 1, 3, 512>{});
+        if (stages == 0) return f(Shape<4, 4, 0, 1024>{});
+        return stages == 3 ? f(Shape<4, 4, 3, 512>{}) : f(Shape<4, 4, 2, 512>{});
+    }
+    return cudaErrorInvalidValue;
+}
+template <typename F>
+cudaError_t by_kind(int kind, F&& f) {
+    return kind == GLA_NORM_RMS ? f(std::integral_constant<int, GLA_NORM_RMS>{})
+                                : f(std::integral_constant<int, GLA_NORM_LAYER>{});
+}
+
+inline bool aligned16(const void* x) { return x == nullptr || (reinterpret_cast<uintptr_t>(x) & 15u) == 0; }
+template <int N>
+bool all_aligned(const void* const (&ptrs)[N]) {
+    for (const void* q : ptrs)
+        if (!aligned16(q)) return false;
+    return true;
+}
+// What both operators ask of a problem.
+inline gla_status check_common(const gla_norm_problem* p) {
+    if (!p || p->B < 0 || p->H < 0 || p->L < 0 || p->D < 1) return GLA_ERR_INVALID_ARG;
+    if (p->io != GLA_F32 && p->io != GLA_BF16) return GLA_ERR_INVALID_ARG;
+    if (p->kind != GLA_NORM_RMS && p->kind != GLA_NORM_LAYER) return GLA_ERR_INVALID_ARG;
+    if (!(p->eps > 0.f) || p->eps > 3.4e38f) return GLA_ERR_INVALID_ARG;
+    if (p->D > 16384 || (long long)p->B * p->L > 2147483647LL) return GLA_ERR_UNSUPPORTED;
+    return GLA_OK;
+}
+
+}  // namespace norm
+}  // namespace gla
