@@ -9,35 +9,67 @@ namespace {
 
 using namespace norm;
 
-// act(z) and its derivative. With bf16 data the exponential is the hardware's (its relative error grows
-// with |z|, 2^-19 at |z| = 25: under a hundredth of the data's rounding); fp32 takes the exact one.
-template <typename T, int ACT>
-__device__ __forceinline__ void act_grad(float z, float& f, float& df) {
-    const float e = std::is_same<T, float>::value ? expf(-z) : __expf(-z);
-    const float p = __fdividef(1.f, 1.f + e);   // 0 where e overflows
-    f = ACT == GLA_ACT_SILU ? z * p : p;
-    df = ACT == GLA_ACT_SILU ? p * fmaf(z, 1.f - p, 1.f) : p * (1.f - p);
-}
-template <typename T, int ACT>
-__device__ __forceinline__ void act_grad2(uint64_t z, uint64_t& f, uint64_t& df) {
-    float z0, z1, f0, f1, d0, d1;
-    f2_split(z, z0, z1);
-    act_grad<T, ACT>(z0, f0, d0);
-    act_grad<T, ACT>(z1, f1, d1);
-    f = f2(f0, f1);
-    df = f2(d0, d1);
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
-// The tokens of one head that a thread's group takes, `step` apart: batch and position advance without
-// divisions.
+// act(z) and its derivative for two channels, from p = 1 / (1 + 2^(-z log2 e)). The product is rounded
+// before the exponential: an error of up to |z| 2^-24 in p, which bf16 data leave at that (2^-19 at
+// |z| = 25, below a hundredth of their rounding) and fp32 data correct by the product's remainder.
+template <typename T, int ACT>
+__device__ __forceinline__ void act_grad2(uint64_t z, uint64_t& f, uint64_t& df) {
+    constexpr float kL = 1.44269502162933349609375f, kLo = 1.92596299e-8f;   // log2 e as a sum
+    const uint64_t y = f2_mul(z, f2_all(-kL));
+    float y0, y1;
+    f2_split(y, y0, y1);
+    uint64_t e = f2(ex2(y0), ex2(y1));
+    if constexpr (std::is_same<T, float>::value) {
+        // beyond |y| = 126 e is 0 or infinite to fp32's purposes, and the remainder may be anything
+        uint64_t rest = f2_fma(z, f2_all(-kLo), f2_fma(z, f2_all(-kL), f2_mul(y, f2_all(-1.f))));
+        float r0, r1;
+        f2_split(rest, r0, r1);
+        rest = f2(fabsf(y0) < 126.f ? r0 : 0.f, fabsf(y1) < 126.f ? r1 : 0.f);
+        e = f2_mul(e, f2_fma(rest, f2_all(0.693147182464599609375f), f2_all(1.f)));
+    }
+    float u0, u1;
+    f2_split(f2_add(e, f2_all(1.f)), u0, u1);
+    const uint64_t p = f2(tc::rcp_approx(u0), tc::rcp_approx(u1));   // 0 where e is infinite
+    const uint64_t q = f2_fma(p, f2_all(-1.f), f2_all(1.f));
+    f = ACT == GLA_ACT_SILU ? f2_mul(z, p) : p;
+    df = ACT == GLA_ACT_SILU ? f2_mul(p, f2_fma(z, q, f2_all(1.f))) : f2_mul(p, q);
+}
+
+// The tokens of one head that a thread's group takes, one every `step`: element offsets of the token in
+// [B,H,L,D] and in [B,L,H,D], advanced without products or divisions.
 struct Token {
-    long long t;
-    int b, l;
-    __device__ __forceinline__ void go(long long step, int sb, int sl, int L) {
-        t += step;
-        b += sb;
-        l += sl;
-        if (l >= L) l -= L, ++b;
+    size_t src, dst;
+    int l;
+};
+struct Walk {
+    size_t dsrc, ddst, wrap;
+    int sl, L;
+    __device__ __forceinline__ Walk(long long step, int H, int L_, int D) : L(L_) {
+        const long long sb = step / L;
+        sl = (int)(step - sb * L);
+        dsrc = ((size_t)sb * H * L + sl) * D;
+        ddst = (size_t)step * H * D;
+        wrap = (size_t)(H - 1) * L * D;   // from the next batch's head 0 to ours, less this batch's tokens
+    }
+    __device__ __forceinline__ Token first(long long t, int h, int H, int D) const {
+        const long long b = t / L;
+        Token k;
+        k.l = (int)(t - b * L);
+        k.src = (((size_t)b * H + h) * L + k.l) * D;
+        k.dst = ((size_t)t * H + h) * D;
+        return k;
+    }
+    __device__ __forceinline__ void go(Token& k) const {
+        k.src += dsrc;
+        k.dst += ddst;
+        k.l += sl;
+        if (k.l >= L) k.l -= L, k.src += wrap;
     }
 };
 
@@ -58,33 +90,27 @@ __global__ void __launch_bounds__(MAXT)
     uint64_t wv[NV][NP];
     load_columns<VEC, NV>(wv, w ? w + (size_t)h * w_stride : nullptr, P, 1.f);
     const long long step = (long long)gridDim.x * ngrp;
-    const int sb = (int)(step / L), sl = (int)(step % L);
-    Token in;   // the next token to copy
-    in.t = (long long)blockIdx.x * ngrp + grp;
-    in.b = (int)(in.t / L);
-    in.l = (int)(in.t % L);
-    auto source = [&](const Token& k) { return o + (((size_t)k.b * H + h) * L + k.l) * D; };
+    long long t = (long long)blockIdx.x * ngrp + grp, ahead = t;
+    const Walk walk(step, H, L, D);
+    Token in = walk.first(t, h, H, D), out = in;   // the next token to copy, the current one
     auto copy = [&](int stage) {
         if (S > 0) {
-            if (in.t < tokens) {
-                const T *os = source(in), *zs = z ? z + ((size_t)in.t * H + h) * D : nullptr;
+            if (ahead < tokens)
 #pragma unroll
                 for (int j = 0; j < NV; ++j)
                     if (P.has(j)) {
-                        feed.template copy<T, VEC>(stage, 0, j, os + P.col<VEC>(j));
-                        if (z) feed.template copy<T, VEC>(stage, ZOFF, j, zs + P.col<VEC>(j));
+                        feed.template copy<T, VEC>(stage, 0, j, o + in.src + P.col<VEC>(j));
+                        if (z) feed.template copy<T, VEC>(stage, ZOFF, j, z + in.dst + P.col<VEC>(j));
                     }
-            }
             feed.commit();
-            in.go(step, sb, sl, L);
+            walk.go(in);
+            ahead += step;
         }
     };
 #pragma unroll
     for (int k = 0; k + 1 < S; ++k) copy(k);
-    long long t = (long long)blockIdx.x * ngrp + grp;
     for (long long first = (long long)blockIdx.x * ngrp; first < tokens; first += step, t += step) {
         const bool live = t < tokens;
-        const size_t dst = ((size_t)t * H + h) * D;
         if (S > 0) {
             feed.wait();
             copy(feed.ahead());
@@ -96,7 +122,7 @@ __global__ void __launch_bounds__(MAXT)
             for (int i = 0; i < NP; ++i) r[j][i] = 0;
             if (live && P.has(j)) {
                 if constexpr (S > 0) feed.template read<T, VEC>(0, j, r[j]);
-                else load_piece<VEC>(source(in) + P.col<VEC>(j), r[j]);
+                else load_piece<VEC>(o + out.src + P.col<VEC>(j), r[j]);
             }
         }
         center<KIND, VEC, NV>(sum, r, P, inv_d);
@@ -111,7 +137,7 @@ __global__ void __launch_bounds__(MAXT)
                 if (z) {
                     uint64_t zv[NP];
                     if constexpr (S > 0) feed.template read<T, VEC>(ZOFF, j, zv);
-                    else load_piece<VEC>(z + dst + P.col<VEC>(j), zv);
+                    else load_piece<VEC>(z + out.dst + P.col<VEC>(j), zv);
 #pragma unroll
                     for (int i = 0; i < NP; ++i) {
                         uint64_t f, df;
@@ -119,10 +145,10 @@ __global__ void __launch_bounds__(MAXT)
                         r[j][i] = f2_mul(r[j][i], f);
                     }
                 }
-                store_piece<VEC>(y + dst + P.col<VEC>(j), r[j]);
+                store_piece<VEC>(y + out.dst + P.col<VEC>(j), r[j]);
             }
         feed.next();
-        if (S == 0) in.go(step, sb, sl, L);
+        walk.go(out);
     }
 }
 
@@ -143,34 +169,28 @@ __global__ void __launch_bounds__(MAXT)
     uint64_t wv[NV][NP], aw[NV][NP] = {};
     load_columns<VEC, NV>(wv, w ? w + (size_t)h * w_stride : nullptr, P, 1.f);
     const long long step = (long long)gridDim.x * ngrp;
-    const int sb = (int)(step / L), sl = (int)(step % L);
-    Token in, out;   // the next token to copy, the current one
-    in.t = (long long)blockIdx.x * ngrp + grp;
-    in.b = (int)(in.t / L);
-    in.l = (int)(in.t % L);
-    out = in;
-    auto place = [&](const Token& k) { return (((size_t)k.b * H + h) * L + k.l) * D; };
+    long long t = (long long)blockIdx.x * ngrp + grp, ahead = t;
+    const Walk walk(step, H, L, D);
+    Token in = walk.first(t, h, H, D), out = in;   // the next token to copy, the current one
     auto copy = [&](int stage) {
         if (S > 0) {
-            if (in.t < tokens) {
-                const size_t src = place(in), dst = ((size_t)in.t * H + h) * D;
+            if (ahead < tokens)
 #pragma unroll
                 for (int j = 0; j < NV; ++j)
                     if (P.has(j)) {
-                        feed.template copy<T, VEC>(stage, 0, j, o + src + P.col<VEC>(j));
-                        feed.template copy<T, VEC>(stage, YOFF, j, dy + dst + P.col<VEC>(j));
-                        if (z) feed.template copy<T, VEC>(stage, ZOFF, j, z + dst + P.col<VEC>(j));
+                        feed.template copy<T, VEC>(stage, 0, j, o + in.src + P.col<VEC>(j));
+                        feed.template copy<T, VEC>(stage, YOFF, j, dy + in.dst + P.col<VEC>(j));
+                        if (z) feed.template copy<T, VEC>(stage, ZOFF, j, z + in.dst + P.col<VEC>(j));
                     }
-            }
             feed.commit();
-            in.go(step, sb, sl, L);
+            walk.go(in);
+            ahead += step;
         }
     };
 #pragma unroll
     for (int k = 0; k + 1 < S; ++k) copy(k);
-    for (long long first = (long long)blockIdx.x * ngrp; first < tokens; first += step) {
-        const bool live = out.t < tokens;
-        const size_t dst = ((size_t)out.t * H + h) * D, src = place(out);
+    for (long long first = (long long)blockIdx.x * ngrp; first < tokens; first += step, t += step) {
+        const bool live = t < tokens;
         if (S > 0) {
             feed.wait();
             copy(feed.ahead());
@@ -182,7 +202,7 @@ __global__ void __launch_bounds__(MAXT)
             for (int i = 0; i < NP; ++i) r[j][i] = 0;
             if (live && P.has(j)) {
                 if constexpr (S > 0) feed.template read<T, VEC>(0, j, r[j]);
-                else load_piece<VEC>(o + src + P.col<VEC>(j), r[j]);
+                else load_piece<VEC>(o + out.src + P.col<VEC>(j), r[j]);
             }
         }
         center<KIND, VEC, NV>(sum, r, P, inv_d);
@@ -194,10 +214,10 @@ __global__ void __launch_bounds__(MAXT)
             if (live && P.has(j)) {
                 uint64_t zv[NP];
                 if constexpr (S > 0) feed.template read<T, VEC>(YOFF, j, q[j]);
-                else load_piece<VEC>(dy + dst + P.col<VEC>(j), q[j]);
+                else load_piece<VEC>(dy + out.dst + P.col<VEC>(j), q[j]);
                 if (z) {
                     if constexpr (S > 0) feed.template read<T, VEC>(ZOFF, j, zv);
-                    else load_piece<VEC>(z + dst + P.col<VEC>(j), zv);
+                    else load_piece<VEC>(z + out.dst + P.col<VEC>(j), zv);
 #pragma unroll
                     for (int i = 0; i < NP; ++i) {
                         uint64_t f, df;
@@ -235,11 +255,11 @@ __global__ void __launch_bounds__(MAXT)
                     r[j][i] = f2_fma(f2_mul(q[j][i], wv[j][i]), rstd2, f2_mul(n, mdn));
                     if (KIND == GLA_NORM_LAYER) r[j][i] = f2_add(r[j][i], md);
                 }
-                if (dz) store_piece<VEC>(dz + dst + P.col<VEC>(j), d[j]);
-                store_piece<VEC>(d_o + src + P.col<VEC>(j), r[j]);
+                if (dz) store_piece<VEC>(dz + out.dst + P.col<VEC>(j), d[j]);
+                store_piece<VEC>(d_o + out.src + P.col<VEC>(j), r[j]);
             }
         feed.next();
-        out.go(step, sb, sl, L);
+        walk.go(out);
     }
     grid_dep_launch();
     if (pdw)

@@ -6,8 +6,7 @@
 //
 // The kernels are bound by HBM, and next by instruction issue (a bf16 element has 10 to 14 bytes of
 // traffic to hide about 30 instructions behind). So a row is read once and held by the G threads that
-// share it, 16 elements a thread where the row is long, so that the row sums' exchange is spread over
-// many elements; arithmetic is on packed pairs of fp32; several sums share their shuffles; and
+// share it, 16 elements a thread, so that the row sums' exchange is spread over many elements; arithmetic is on packed pairs of fp32; several sums share their shuffles; and
 // every thread copies its own pieces of the next rows into shared memory asynchronously (a ring that only
 // its own thread reads, so no barrier guards it). Rows of up to 512 elements belong to a warp or
 // less, longer ones to a block. Blocks walk many rows and keep the column sums (dw) in registers.
@@ -355,9 +354,9 @@ inline cudaError_t colsum(const float* part0, float* out0, const float* part1, f
 // Threads and pieces of a row. A piece is 16 bytes of the widest type in the row (8 bf16, or 4 where
 // fp32 stands beside them: with 8 the fp32 accesses of a warp would leave every other 16 bytes out,
 // 305 instead of 224 us for the backward of 16384 x 4096 with an fp32 residual), 4 elements where D is
-// no multiple of 8, one where it is odd. One piece a thread while a warp's lanes hold the row,
-// 16 elements a thread beyond (4 for single elements up to D = 2048); a power of two of lanes up to a
-// warp (D <= 512), whole warps beyond.
+// no multiple of 8, one where it is no multiple of 4. A thread holds 16 elements, so that the row sums'
+// exchange and the addresses of a row are spread over many (4 for single elements up to D = 2048); a
+// row has a power of two of lanes up to a warp (D <= 512), whole warps beyond.
 struct RowPlan {
     int vec, nv, G, threads;
     bool big;   // more than 512 threads: D > 8192
@@ -366,7 +365,7 @@ inline RowPlan row_plan(int D, bool all_bf16) {
     RowPlan p;
     p.vec = all_bf16 && D % 8 == 0 ? 8 : D % 4 == 0 ? 4 : 1;
     const int nvec = D / p.vec;
-    p.nv = nvec <= 32 ? 1 : p.vec == 1 && D <= 2048 ? 4 : 16 / p.vec;
+    p.nv = p.vec == 1 && D <= 2048 ? 4 : 16 / p.vec;
     const int need = cdiv(nvec, p.nv);
     if (need > 32) {
         p.G = cdiv(need, 32) * 32;
@@ -388,7 +387,7 @@ inline int ring_stages(const RowPlan& p, int thread_bytes) {
     const int row = thread_bytes * p.threads;
     if (p.vec == 1 || p.big) return 0;
     if (2 * (3 * row + kHead + 1024) <= kSmSmem) return 3;
-    return p.nv > 1 && 2 * row + kHead + 1024 <= kSmSmem ? 2 : 0;
+    return 2 * row + kHead + 1024 <= kSmSmem ? 2 : 0;
 }
 inline size_t block_smem(const RowPlan& p, int stages, int thread_bytes) {
     const size_t ring = kHead + (size_t)stages * thread_bytes * p.threads;
@@ -428,16 +427,13 @@ cudaError_t by_shape(const RowPlan& p, int stages, F&& f) {
     constexpr int W = BF16 ? 8 : 4;
     if (p.vec == 1) {
         if (p.big) return f(Shape<1, 16, 0, 1024>{});
-        if (p.nv == 1) return f(Shape<1, 1, 0, 512>{});
         return p.nv == 4 ? f(Shape<1, 4, 0, 512>{}) : f(Shape<1, 16, 0, 512>{});
     }
     if (p.vec == W) {
-        if (p.nv == 1) return f(Shape<W, 1, 3, 512>{});
         if (stages == 0) return f(Shape<W, 16 / W, 0, 1024>{});
         return stages == 3 ? f(Shape<W, 16 / W, 3, 512>{}) : f(Shape<W, 16 / W, 2, 512>{});
     }
     if constexpr (W == 8) {   // D a multiple of 4 only
-        if (p.nv == 1) return f(Shape<4, 1, 3, 512>{});
         if (stages == 0) return f(Shape<4, 4, 0, 1024>{});
         return stages == 3 ? f(Shape<4, 4, 3, 512>{}) : f(Shape<4, 4, 2, 512>{});
     }
