@@ -338,10 +338,11 @@ GLA_API gla_status gla_mlstm_bwd_saved(const gla_problem* p, const void* q, cons
  *   the backward reads them instead of running the recurrence once more. `saved` must come from
  *   gla_scan_fwd_save with the same problem, input and x, g, h0; NULL means recompute (the same
  *   as gla_scan_bwd).
- * ws: caller-owned device workspace of gla_scan_workspace_bytes(p, for_backward) bytes (0 when p
- *   is invalid or unsupported). There is no device status word in it; the kernels' waits on their
- *   own copies are bounded, and one that gave up (a fault elsewhere on the device) ends the call
- *   with results that are not valid rather than hanging.
+ * ws: the backward's caller-owned device workspace of gla_scan_bwd_workspace_bytes(p) bytes (0 when p
+ *   is invalid or unsupported), for the states; with `saved` none is needed (NULL, 0). There is
+ *   no device status word; the kernels' waits on their own copies are bounded, and one that
+ *   gave up (a fault elsewhere on the device) ends the call with results that are not valid
+ *   rather than hanging.
  * Outputs may not overlap inputs, saved or ws. All pointers 16-byte aligned device memory.
  * Errors: GLA_ERR_INVALID_ARG (null or misaligned pointer, bad enum, sizes, a gate mode),
  *   GLA_ERR_UNSUPPORTED (D, L, B * H), GLA_ERR_WORKSPACE, GLA_ERR_CUDA. */
@@ -350,15 +351,15 @@ typedef enum {
     GLA_SCAN_COMPLEMENT = 1, /* m = 1 - alpha */
     GLA_SCAN_NORM = 2        /* m = sqrt(1 - alpha^2) */
 } gla_scan_input;
-GLA_API size_t gla_scan_workspace_bytes(const gla_problem* p, int for_backward);
+GLA_API size_t gla_scan_bwd_workspace_bytes(const gla_problem* p);
 GLA_API size_t gla_scan_saved_bytes(const gla_problem* p);
 GLA_API gla_status gla_scan_fwd(const gla_problem* p, int input, const void* x, const float* g, const float* h0,
-                                void* o, float* hT, void* ws, size_t ws_bytes, void* stream);
+                                void* o, float* hT, void* stream);
 GLA_API gla_status gla_scan_bwd(const gla_problem* p, int input, const void* x, const float* g, const float* h0,
                                 const void* dO, const float* dhT, void* dx, float* dg, float* dh0, void* ws,
                                 size_t ws_bytes, void* stream);
 GLA_API gla_status gla_scan_fwd_save(const gla_problem* p, int input, const void* x, const float* g, const float* h0,
-                                     void* o, float* hT, float* saved, void* ws, size_t ws_bytes, void* stream);
+                                     void* o, float* hT, float* saved, void* stream);
 GLA_API gla_status gla_scan_bwd_saved(const gla_problem* p, int input, const void* x, const float* g,
                                       const float* h0, const void* dO, const float* dhT, const float* saved,
                                       void* dx, float* dg, float* dh0, void* ws, size_t ws_bytes, void* stream);

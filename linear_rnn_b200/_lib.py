@@ -28,7 +28,7 @@ EXPORTED = ("gla_workspace_bytes", "gla_fwd", "gla_bwd", "gla_status_string",
             "gla_deltanet_bwd_workspace_bytes", "gla_deltanet_bwd", "gla_mlstm_workspace_bytes", "gla_mlstm_fwd",
             "gla_mlstm_bwd", "gla_shard_workspace_bytes", "gla_deltanet_saved_bytes", "gla_deltanet_fwd_save",
             "gla_deltanet_bwd_saved", "gla_mlstm_saved_bytes", "gla_mlstm_fwd_save", "gla_mlstm_bwd_saved",
-            "gla_scan_workspace_bytes", "gla_scan_saved_bytes", "gla_scan_fwd", "gla_scan_bwd", "gla_scan_fwd_save",
+            "gla_scan_bwd_workspace_bytes", "gla_scan_saved_bytes", "gla_scan_fwd", "gla_scan_bwd", "gla_scan_fwd_save",
             "gla_scan_bwd_saved", "gla_scan_decode", "gla_addnorm_workspace_bytes", "gla_addnorm_fwd",
             "gla_addnorm_bwd", "gla_headnorm_workspace_bytes", "gla_headnorm_fwd", "gla_headnorm_bwd")
 
@@ -122,13 +122,13 @@ def _load():
     lib.gla_mlstm_bwd_saved.argtypes = [pp] + [ctypes.c_void_p] * 13 + [ctypes.c_size_t, ctypes.c_void_p]
     lib.gla_mlstm_bwd_saved.restype = ctypes.c_int
     np_ = ctypes.POINTER(GlaNormProblem)
-    lib.gla_scan_workspace_bytes.argtypes = [pp, ctypes.c_int]
-    lib.gla_scan_workspace_bytes.restype = ctypes.c_size_t
+    lib.gla_scan_bwd_workspace_bytes.argtypes = [pp]
+    lib.gla_scan_bwd_workspace_bytes.restype = ctypes.c_size_t
     lib.gla_scan_saved_bytes.argtypes = [pp]
     lib.gla_scan_saved_bytes.restype = ctypes.c_size_t
-    lib.gla_scan_fwd.argtypes = [pp, ctypes.c_int] + [ctypes.c_void_p] * 6 + [ctypes.c_size_t, ctypes.c_void_p]
+    lib.gla_scan_fwd.argtypes = [pp, ctypes.c_int] + [ctypes.c_void_p] * 6
     lib.gla_scan_bwd.argtypes = [pp, ctypes.c_int] + [ctypes.c_void_p] * 9 + [ctypes.c_size_t, ctypes.c_void_p]
-    lib.gla_scan_fwd_save.argtypes = [pp, ctypes.c_int] + [ctypes.c_void_p] * 7 + [ctypes.c_size_t, ctypes.c_void_p]
+    lib.gla_scan_fwd_save.argtypes = [pp, ctypes.c_int] + [ctypes.c_void_p] * 7
     lib.gla_scan_bwd_saved.argtypes = [pp, ctypes.c_int] + [ctypes.c_void_p] * 10 + [ctypes.c_size_t, ctypes.c_void_p]
     lib.gla_scan_decode.argtypes = [pp, ctypes.c_int] + [ctypes.c_void_p] * 5
     lib.gla_addnorm_workspace_bytes.argtypes = [np_]

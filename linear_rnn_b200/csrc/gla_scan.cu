@@ -763,27 +763,26 @@ size_t gla_scan_saved_bytes(const gla_problem* p) {
     return 4 * (size_t)p->B * p->H * cdiv(p->L, kSaveEvery) * p->Dk;
 }
 
-size_t gla_scan_workspace_bytes(const gla_problem* p, int for_backward) {
+size_t gla_scan_bwd_workspace_bytes(const gla_problem* p) {
     if (check(p) != GLA_OK) return 0;
-    return for_backward ? align_up(gla_scan_saved_bytes(p), 256) + 256 : 256;
+    return align_up(gla_scan_saved_bytes(p), 256) + 256;
 }
 
 gla_status gla_scan_fwd(const gla_problem* p, int input, const void* x, const float* g, const float* h0, void* o,
-                        float* hT, void* ws, size_t ws_bytes, void* stream) {
-    return gla_scan_fwd_save(p, input, x, g, h0, o, hT, nullptr, ws, ws_bytes, stream);
+                        float* hT, void* stream) {
+    return gla_scan_fwd_save(p, input, x, g, h0, o, hT, nullptr, stream);
 }
 
 gla_status gla_scan_fwd_save(const gla_problem* p, int input, const void* x, const float* g, const float* h0, void* o,
-                             float* hT, float* saved, void* ws, size_t ws_bytes, void* stream) {
+                             float* hT, float* saved, void* stream) {
     const gla_status s = check(p);
     if (s != GLA_OK) return s;
-    if (!input_ok(input) || !ws) return GLA_ERR_INVALID_ARG;
+    if (!input_ok(input)) return GLA_ERR_INVALID_ARG;
     const bool empty = (size_t)p->B * p->H * p->L == 0;
     if (!empty && (!x || !g || !o)) return GLA_ERR_INVALID_ARG;
-    const void* ptrs[] = {x, g, h0, o, hT, saved, ws};
+    const void* ptrs[] = {x, g, h0, o, hT, saved};
     for (const void* q : ptrs)
         if (!aligned16(q)) return GLA_ERR_INVALID_ARG;
-    if (ws_bytes < gla_scan_workspace_bytes(p, 0)) return GLA_ERR_WORKSPACE;
     if ((size_t)p->B * p->H == 0) return GLA_OK;
     return record_cuda(fwd(p, input, x, g, h0, o, hT, saved, (cudaStream_t)stream), "scan forward");
 }
@@ -799,13 +798,13 @@ gla_status gla_scan_bwd_saved(const gla_problem* p, int input, const void* x, co
                               void* ws, size_t ws_bytes, void* stream) {
     const gla_status s = check(p);
     if (s != GLA_OK) return s;
-    if (!input_ok(input) || !ws) return GLA_ERR_INVALID_ARG;
+    if (!input_ok(input) || (!saved && !ws)) return GLA_ERR_INVALID_ARG;
     const bool empty = (size_t)p->B * p->H * p->L == 0;
     if (!empty && (!x || !g || !dO || !dx || !dg)) return GLA_ERR_INVALID_ARG;
     const void* ptrs[] = {x, g, h0, dO, dhT, saved, dx, dg, dh0, ws};
     for (const void* q : ptrs)
         if (!aligned16(q)) return GLA_ERR_INVALID_ARG;
-    if (ws_bytes < gla_scan_workspace_bytes(p, 1)) return GLA_ERR_WORKSPACE;
+    if (!saved && ws_bytes < gla_scan_bwd_workspace_bytes(p)) return GLA_ERR_WORKSPACE;
     if ((size_t)p->B * p->H == 0) return GLA_OK;
     cudaStream_t st = (cudaStream_t)stream;
     if (!saved) {

@@ -300,6 +300,10 @@ def gla_deltanet_bwd(q, k, v, beta, h0, dO, dhT=None, *, scale: Optional[float] 
     return out
 
 
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
 def _take(name, t, shape, dtype, device):
     """A checked argument on `device`: `shape` and `dtype` exactly, contiguous, or None."""
     if t is None:
@@ -307,7 +311,7 @@ def _take(name, t, shape, dtype, device):
     if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
     if t.device != device:
-        if t.device.type == "cuda":
+        if t.is_cuda:
             raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
         t = t.to(device, non_blocking=True)
     if not t.is_contiguous():
@@ -315,38 +319,33 @@ def _take(name, t, shape, dtype, device):
     return t
 
 
+def _need(name, t, shape, dtype, device):
+    if t is None:
+        raise ValueError(f"{name} is needed")
+    return _take(name, t, shape, dtype, device)
+
+
 def _choice(name, value, table):
-    if value not in table:
+    got = table.get(value)
+    if got is None:
         raise ValueError(f"{name} must be one of {sorted(table)}")
-    return table[value]
+    return got
 
 
-def _call(fn, device, *args):
-    """Launches on the current stream of `device`, with that device current."""
-    if device.index == torch.cuda.current_device():
-        return fn(*args, _stream_handle(device))
-    with torch.cuda.device(device):
-        return fn(*args, _stream_handle(device))
+def _launch(where, fn, device, *args):
+    """Calls fn with the current stream of `device`, with that device current."""
+    i = device.index
+    if i == torch.cuda.current_device():
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(i))
+    else:
+        with torch.cuda.device(i):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(i))
+    if st != _lib.GLA_OK:
+        raise GlaError(st, where)
 
 
 def _device_of(t):
-    return torch.device("cuda", torch.cuda.current_device()) if t.device.type != "cuda" else t.device
-
-
-def make_scan_problem(x: torch.Tensor) -> GlaProblem:
-    """The gla_problem of the vector-state recurrence over x [B,H,L,D]."""
-    if x.dim() != 4:
-        raise ValueError("x must be [B, H, L, D]")
-    B, H, L, D = x.shape
-    return GlaProblem(B, H, L, D, D, 64, 1.0, _io_dtype(x.dtype), _lib.GLA_GATE_PER_KEY, _lib.GLA_PLAN_AUTO)
-
-
-def gla_scan_saved_bytes(problem: GlaProblem) -> int:
-    return int(_lib.lib.gla_scan_saved_bytes(ctypes.byref(problem)))
-
-
-def gla_scan_workspace_bytes(problem: GlaProblem, for_backward: bool) -> int:
-    return int(_lib.lib.gla_scan_workspace_bytes(ctypes.byref(problem), int(for_backward)))
+    return t.device if t.is_cuda else torch.device("cuda", torch.cuda.current_device())
 
 
 def _buffer(name, t, nbytes, device):
@@ -366,8 +365,23 @@ def _work_buffer(workspace, nbytes, device, where):
     return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
+def make_scan_problem(x: torch.Tensor) -> GlaProblem:
+    """The gla_problem of the vector-state recurrence over x [B,H,L,D]."""
+    if x.dim() != 4:
+        raise ValueError("x must be [B, H, L, D]")
+    B, H, L, D = x.shape
+    return GlaProblem(B, H, L, D, D, 64, 1.0, _io_dtype(x.dtype), _lib.GLA_GATE_PER_KEY, _lib.GLA_PLAN_AUTO)
+
+
+def gla_scan_saved_bytes(problem: GlaProblem) -> int:
+    return _lib.lib.gla_scan_saved_bytes(ctypes.byref(problem))
+
+
+def gla_scan_bwd_workspace_bytes(problem: GlaProblem) -> int:
+    return _lib.lib.gla_scan_bwd_workspace_bytes(ctypes.byref(problem))
+
+
 def gla_scan_fwd(x, g, h0=None, *, input: str = "plain", output_final_state: bool = True,
-                 workspace: Optional[torch.Tensor] = None,
                  saved_states: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """Gated linear recurrence with a vector state, h_t = e^{g_t} h_{t-1} + m(g_t) x_t per channel:
     x [B,H,L,D] (bf16 or fp32), g [B,H,L,D] fp32 (log-decay; -inf starts anew), h0 [B,H,D] fp32 or
@@ -376,22 +390,19 @@ def gla_scan_fwd(x, g, h0=None, *, input: str = "plain", output_final_state: boo
     saved_states: optional device buffer (at least gla_scan_saved_bytes) that receives the states
     entering every 64 tokens, for gla_scan_bwd(..., saved_states=). Host tensors are copied to the
     current device and the results back."""
-    host, device = x.device.type != "cuda", _device_of(x)
-    prob, mode = make_scan_problem(x), _choice("input", input, _SCAN_INPUTS)
-    x = _take("x", x, x.shape, x.dtype, device)
-    g = _take("g", g, x.shape, torch.float32, device)
-    if g is None:
-        raise ValueError("g is needed")
-    ends = x.shape[:2] + x.shape[3:]
+    device = _device_of(x)
+    prob, mode, shape = make_scan_problem(x), _choice("input", input, _SCAN_INPUTS), x.shape
+    ends = (shape[0], shape[1], shape[3])
+    host = not x.is_cuda
+    x = _take("x", x, shape, x.dtype, device)
+    g = _need("g", g, shape, torch.float32, device)
     h0 = _take("h0", h0, ends, torch.float32, device)
-    ws = _work_buffer(workspace, gla_scan_workspace_bytes(prob, False), device, "gla_scan_workspace_bytes")
     if saved_states is not None:
         _buffer("saved_states", saved_states, gla_scan_saved_bytes(prob), device)
     o = torch.empty_like(x)
     hT = torch.empty(ends, dtype=torch.float32, device=device) if output_final_state else None
-    st = _call(_lib.lib.gla_scan_fwd_save, device, ctypes.byref(prob), mode, _ptr(x), _ptr(g), _ptr(h0), _ptr(o),
-               _ptr(hT), _ptr(saved_states), _ptr(ws), ws.numel() * ws.element_size())
-    _check(st, "gla_scan_fwd")
+    _launch("gla_scan_fwd", _lib.lib.gla_scan_fwd_save, device, ctypes.byref(prob), mode, _addr(x), _addr(g),
+            _addr(h0), _addr(o), _addr(hT), _addr(saved_states))
     if host:
         o, hT = _to_host([o, hT])
     return o, hT
@@ -402,26 +413,27 @@ def gla_scan_bwd(x, g, h0, dO, dhT=None, *, input: str = "plain", output_dh0: bo
                  saved_states: Optional[torch.Tensor] = None) -> Dict[str, Optional[torch.Tensor]]:
     """Gradients of sum(dO * o) + sum(dhT * hT) of gla_scan_fwd: dict dx (io dtype), dg (fp32) and
     dh0 (fp32, or None when output_dh0 is False). saved_states: the buffer a gla_scan_fwd on the
-    same x, g, h0 and input filled, or None to run the recurrence again."""
-    host, device = x.device.type != "cuda", _device_of(x)
-    prob, mode = make_scan_problem(x), _choice("input", input, _SCAN_INPUTS)
-    x = _take("x", x, x.shape, x.dtype, device)
-    g = _take("g", g, x.shape, torch.float32, device)
-    dO = _take("dO", dO, x.shape, x.dtype, device)
-    if g is None or dO is None:
-        raise ValueError("g and dO are needed")
-    ends = x.shape[:2] + x.shape[3:]
+    same x, g, h0 and input filled, or None to run the recurrence again (which needs a workspace
+    of gla_scan_bwd_workspace_bytes, allocated when None)."""
+    device = _device_of(x)
+    prob, mode, shape = make_scan_problem(x), _choice("input", input, _SCAN_INPUTS), x.shape
+    ends = (shape[0], shape[1], shape[3])
+    host = not x.is_cuda
+    x = _take("x", x, shape, x.dtype, device)
+    g = _need("g", g, shape, torch.float32, device)
+    dO = _need("dO", dO, shape, x.dtype, device)
     h0 = _take("h0", h0, ends, torch.float32, device)
     dhT = _take("dhT", dhT, ends, torch.float32, device)
-    ws = _work_buffer(workspace, gla_scan_workspace_bytes(prob, True), device, "gla_scan_workspace_bytes")
+    ws, nbytes = None, 0
     if saved_states is not None:
         _buffer("saved_states", saved_states, gla_scan_saved_bytes(prob), device)
+    else:
+        nbytes = gla_scan_bwd_workspace_bytes(prob)
+        ws = _work_buffer(workspace, nbytes, device, "gla_scan_bwd_workspace_bytes")
     dx, dg = torch.empty_like(x), torch.empty_like(g)
     dh0 = torch.empty(ends, dtype=torch.float32, device=device) if output_dh0 else None
-    st = _call(_lib.lib.gla_scan_bwd_saved, device, ctypes.byref(prob), mode, _ptr(x), _ptr(g), _ptr(h0), _ptr(dO),
-               _ptr(dhT), _ptr(saved_states), _ptr(dx), _ptr(dg), _ptr(dh0), _ptr(ws),
-               ws.numel() * ws.element_size())
-    _check(st, "gla_scan_bwd")
+    _launch("gla_scan_bwd", _lib.lib.gla_scan_bwd_saved, device, ctypes.byref(prob), mode, _addr(x), _addr(g),
+            _addr(h0), _addr(dO), _addr(dhT), _addr(saved_states), _addr(dx), _addr(dg), _addr(dh0), _addr(ws), nbytes)
     if host:
         dx, dg, dh0 = _to_host([dx, dg, dh0])
     return {"dx": dx, "dg": dg, "dh0": dh0}
@@ -430,20 +442,18 @@ def gla_scan_bwd(x, g, h0, dO, dhT=None, *, input: str = "plain", output_dh0: bo
 def gla_scan_decode(x, g, state, *, input: str = "plain") -> torch.Tensor:
     """One token of gla_scan_fwd per (b, h) from `state` (fp32 [B,H,D] on the GPU, updated in
     place): x, g [B,H,1,D]. Returns o [B,H,1,D]."""
-    if state.device.type != "cuda" or state.dtype != torch.float32 or not state.is_contiguous():
+    if not state.is_cuda or state.dtype != torch.float32 or not state.is_contiguous():
         raise ValueError("state must be a contiguous float32 CUDA tensor (it is updated in place)")
     device = state.device
-    prob, mode = make_scan_problem(x), _choice("input", input, _SCAN_INPUTS)
-    if x.shape[2] != 1:
+    prob, mode, shape = make_scan_problem(x), _choice("input", input, _SCAN_INPUTS), x.shape
+    if shape[2] != 1:
         raise ValueError("gla_scan_decode takes one token per (b, h): x must be [B, H, 1, D]")
-    x = _take("x", x, x.shape, x.dtype, device)
-    g = _take("g", g, x.shape, torch.float32, device)
-    if g is None:
-        raise ValueError("g is needed")
-    _take("state", state, x.shape[:2] + x.shape[3:], torch.float32, device)
+    x = _take("x", x, shape, x.dtype, device)
+    g = _need("g", g, shape, torch.float32, device)
+    _take("state", state, (shape[0], shape[1], shape[3]), torch.float32, device)
     o = torch.empty_like(x)
-    st = _call(_lib.lib.gla_scan_decode, device, ctypes.byref(prob), mode, _ptr(x), _ptr(g), _ptr(state), _ptr(o))
-    _check(st, "gla_scan_decode")
+    _launch("gla_scan_decode", _lib.lib.gla_scan_decode, device, ctypes.byref(prob), mode, x.data_ptr(), g.data_ptr(),
+            state.data_ptr(), o.data_ptr())
     return o
 
 
@@ -453,10 +463,11 @@ def _addnorm_problem(x, res_dtype, kind, eps, alpha) -> GlaNormProblem:
     D = x.shape[-1]
     if D < 1:
         raise ValueError("x must have channels")
-    if x.numel() // D > 2147483647:
+    rows = x.numel() // D
+    if rows > 2147483647:
         raise GlaError(_lib.GLA_ERR_UNSUPPORTED, "rows")
-    return GlaNormProblem(1, 1, x.numel() // D, D, _io_dtype(x.dtype), _io_dtype(res_dtype),
-                          _choice("kind", kind, _NORM_KINDS), _lib.GLA_ACT_SILU, 0, float(eps), float(alpha))
+    return GlaNormProblem(1, 1, rows, D, _io_dtype(x.dtype), _io_dtype(res_dtype), _choice("kind", kind, _NORM_KINDS),
+                          _lib.GLA_ACT_SILU, 0, eps, alpha)
 
 
 def gla_addnorm_fwd(x, res=None, w=None, *, rscale=None, alpha: float = 1.0, kind: str = "rms", eps: float = 1e-6,
@@ -467,19 +478,18 @@ def gla_addnorm_fwd(x, res=None, w=None, *, rscale=None, alpha: float = 1.0, kin
     None (one); kind "rms" or "layer". Returns r (res's dtype) and y (x's dtype); y is the norm of
     the fp32 sum, before r is rounded. Host tensors are copied to the current device and the
     results back."""
-    host, device = x.device.type != "cuda", _device_of(x)
+    device, host, shape = _device_of(x), not x.is_cuda, x.shape
     if res is not None and res_dtype not in (None, res.dtype):
         raise ValueError("res_dtype is res's dtype when res is given")
     res_dtype = res.dtype if res is not None else (res_dtype or x.dtype)
     prob = _addnorm_problem(x, res_dtype, kind, eps, alpha)
-    x = _take("x", x, x.shape, x.dtype, device)
-    res = _take("res", res, x.shape, res_dtype, device)
-    w = _take("w", w, x.shape[-1:], torch.float32, device)
-    rscale = _take("rscale", rscale, x.shape[-1:], torch.float32, device)
-    r, y = torch.empty(x.shape, dtype=res_dtype, device=device), torch.empty_like(x)
-    st = _call(_lib.lib.gla_addnorm_fwd, device, ctypes.byref(prob), _ptr(x), _ptr(res), _ptr(rscale), _ptr(w),
-               _ptr(r), _ptr(y))
-    _check(st, "gla_addnorm_fwd")
+    x = _take("x", x, shape, x.dtype, device)
+    res = _take("res", res, shape, res_dtype, device)
+    w = _take("w", w, shape[-1:], torch.float32, device)
+    rscale = _take("rscale", rscale, shape[-1:], torch.float32, device)
+    r, y = torch.empty(shape, dtype=res_dtype, device=device), torch.empty_like(x)
+    _launch("gla_addnorm_fwd", _lib.lib.gla_addnorm_fwd, device, ctypes.byref(prob), _addr(x), _addr(res),
+            _addr(rscale), _addr(w), _addr(r), _addr(y))
     if host:
         r, y = _to_host([r, y])
     return r, y
@@ -492,27 +502,24 @@ def gla_addnorm_bwd(x, r, w, dy, dr=None, *, rscale=None, alpha: float = 1.0, ki
     dtype it equals dres), dw (fp32 [D], None without w) and drscale (fp32 [D], None without
     rscale). x is only read for drscale and may be None without rscale; dr [..., D] is the
     gradient that reaches r from later blocks, or None."""
-    host, device = dy.device.type != "cuda", _device_of(dy)
+    device, host, shape = _device_of(dy), not dy.is_cuda, dy.shape
     prob = _addnorm_problem(dy, r.dtype, kind, eps, alpha)
-    D = dy.shape[-1:]
-    dy = _take("dy", dy, dy.shape, dy.dtype, device)
-    r = _take("r", r, dy.shape, r.dtype, device)
-    dr = _take("dr", dr, dy.shape, r.dtype, device)
+    D = shape[-1:]
+    dy = _take("dy", dy, shape, dy.dtype, device)
+    r = _take("r", r, shape, r.dtype, device)
+    dr = _take("dr", dr, shape, r.dtype, device)
     w = _take("w", w, D, torch.float32, device)
     rscale = _take("rscale", rscale, D, torch.float32, device)
-    if rscale is not None and x is None:
-        raise ValueError("x is needed for rscale's gradient")
-    x = _take("x", x, dy.shape, dy.dtype, device) if rscale is not None else None
-    ws = _work_buffer(workspace, int(_lib.lib.gla_addnorm_workspace_bytes(ctypes.byref(prob))), device,
-                      "gla_addnorm_workspace_bytes")
+    x = _need("x (for rscale's gradient)", x, shape, dy.dtype, device) if rscale is not None else None
+    nbytes = _lib.lib.gla_addnorm_workspace_bytes(ctypes.byref(prob))
+    ws = _work_buffer(workspace, nbytes, device, "gla_addnorm_workspace_bytes")
     dres = torch.empty_like(r)
     dx = torch.empty_like(dy) if output_dx else None
     dw = torch.empty_like(w) if w is not None else None
     ds = torch.empty_like(rscale) if rscale is not None else None
-    st = _call(_lib.lib.gla_addnorm_bwd, device, ctypes.byref(prob), _ptr(x), _ptr(r), _ptr(rscale), _ptr(w),
-               _ptr(dy), _ptr(dr), _ptr(dres), _ptr(dx), _ptr(dw), _ptr(ds), _ptr(ws),
-               ws.numel() * ws.element_size())
-    _check(st, "gla_addnorm_bwd")
+    _launch("gla_addnorm_bwd", _lib.lib.gla_addnorm_bwd, device, ctypes.byref(prob), _addr(x), _addr(r),
+            _addr(rscale), _addr(w), _addr(dy), _addr(dr), _addr(dres), _addr(dx), _addr(dw), _addr(ds), _addr(ws),
+            nbytes)
     out = {"dres": dres, "dx": dx, "dw": dw, "drscale": ds}
     if host:
         out = dict(zip(out, _to_host(list(out.values()))))
@@ -523,9 +530,9 @@ def _headnorm_problem(o, w, act, kind, eps) -> GlaNormProblem:
     if o.dim() != 4:
         raise ValueError("o must be [B, H, L, D]")
     B, H, L, D = o.shape
-    per_head = 1 if w is not None and w.dim() == 2 else 0
-    return GlaNormProblem(B, H, L, D, _io_dtype(o.dtype), _io_dtype(o.dtype), _choice("kind", kind, _NORM_KINDS),
-                          _choice("act", act, _ACTS), per_head, float(eps), 1.0)
+    io = _io_dtype(o.dtype)
+    return GlaNormProblem(B, H, L, D, io, io, _choice("kind", kind, _NORM_KINDS), _choice("act", act, _ACTS),
+                          1 if w is not None and w.dim() == 2 else 0, eps, 1.0)
 
 
 def gla_headnorm_fwd(o, z=None, w=None, *, act: str = "silu", kind: str = "rms", eps: float = 1e-6) -> torch.Tensor:
@@ -534,15 +541,15 @@ def gla_headnorm_fwd(o, z=None, w=None, *, act: str = "silu", kind: str = "rms",
     act ("silu" or "sigmoid"), None: no gate; w fp32 [D] (shared by the heads) or [H,D], None: one;
     kind "rms" or "layer". Returns y [B,L,H,D]: y.view(B, L, H * D) is the out-projection's input.
     Host tensors are copied to the current device and the result back."""
-    host, device = o.device.type != "cuda", _device_of(o)
+    device, host = _device_of(o), not o.is_cuda
     prob = _headnorm_problem(o, w, act, kind, eps)
-    o = _take("o", o, o.shape, o.dtype, device)
     B, H, L, D = o.shape
-    z = _take("z", z, torch.Size((B, L, H, D)), o.dtype, device)
-    w = _take("w", w, torch.Size((H, D) if prob.w_per_head else (D,)), torch.float32, device)
-    y = torch.empty(B, L, H, D, dtype=o.dtype, device=device)
-    st = _call(_lib.lib.gla_headnorm_fwd, device, ctypes.byref(prob), _ptr(o), _ptr(z), _ptr(w), _ptr(y))
-    _check(st, "gla_headnorm_fwd")
+    o = _take("o", o, o.shape, o.dtype, device)
+    z = _take("z", z, (B, L, H, D), o.dtype, device)
+    w = _take("w", w, (H, D) if prob.w_per_head else (D,), torch.float32, device)
+    y = torch.empty((B, L, H, D), dtype=o.dtype, device=device)
+    _launch("gla_headnorm_fwd", _lib.lib.gla_headnorm_fwd, device, ctypes.byref(prob), _addr(o), _addr(z), _addr(w),
+            _addr(y))
     if host:
         (y,) = _to_host([y])
     return y
@@ -552,23 +559,20 @@ def gla_headnorm_bwd(o, z, w, dy, *, act: str = "silu", kind: str = "rms", eps: 
                      workspace: Optional[torch.Tensor] = None) -> Dict[str, Optional[torch.Tensor]]:
     """Gradients of sum(dy * y) of gla_headnorm_fwd: dict do [B,H,L,D], dz [B,L,H,D] (None without
     z), dw (fp32, shaped like w; None without w)."""
-    host, device = o.device.type != "cuda", _device_of(o)
+    device, host = _device_of(o), not o.is_cuda
     prob = _headnorm_problem(o, w, act, kind, eps)
-    o = _take("o", o, o.shape, o.dtype, device)
     B, H, L, D = o.shape
-    z = _take("z", z, torch.Size((B, L, H, D)), o.dtype, device)
-    dy = _take("dy", dy, torch.Size((B, L, H, D)), o.dtype, device)
-    if dy is None:
-        raise ValueError("dy is needed")
-    w = _take("w", w, torch.Size((H, D) if prob.w_per_head else (D,)), torch.float32, device)
-    ws = _work_buffer(workspace, int(_lib.lib.gla_headnorm_workspace_bytes(ctypes.byref(prob))), device,
-                      "gla_headnorm_workspace_bytes")
+    o = _take("o", o, o.shape, o.dtype, device)
+    z = _take("z", z, (B, L, H, D), o.dtype, device)
+    dy = _need("dy", dy, (B, L, H, D), o.dtype, device)
+    w = _take("w", w, (H, D) if prob.w_per_head else (D,), torch.float32, device)
+    nbytes = _lib.lib.gla_headnorm_workspace_bytes(ctypes.byref(prob))
+    ws = _work_buffer(workspace, nbytes, device, "gla_headnorm_workspace_bytes")
     d_o = torch.empty_like(o)
     dz = torch.empty_like(z) if z is not None else None
     dw = torch.empty_like(w) if w is not None else None
-    st = _call(_lib.lib.gla_headnorm_bwd, device, ctypes.byref(prob), _ptr(o), _ptr(z), _ptr(w), _ptr(dy), _ptr(d_o),
-               _ptr(dz), _ptr(dw), _ptr(ws), ws.numel() * ws.element_size())
-    _check(st, "gla_headnorm_bwd")
+    _launch("gla_headnorm_bwd", _lib.lib.gla_headnorm_bwd, device, ctypes.byref(prob), _addr(o), _addr(z), _addr(w),
+            _addr(dy), _addr(d_o), _addr(dz), _addr(dw), _addr(ws), nbytes)
     out = {"do": d_o, "dz": dz, "dw": dw}
     if host:
         out = dict(zip(out, _to_host(list(out.values()))))

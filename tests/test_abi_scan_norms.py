@@ -26,10 +26,10 @@ BAD_SCAN = [(dict(B=-1), INVALID), (dict(L=-1), INVALID), (dict(D=0), INVALID), 
 
 
 def scan_fwd(p, input=0, **kw):
-    a = dict(x=16, g=16, h0=None, o=16, hT=None, saved=None, ws=16, nbytes=1 << 40)
+    a = dict(x=16, g=16, h0=None, o=16, hT=None, saved=None)
     a.update(kw)
-    return lib.gla_scan_fwd_save(ctypes.byref(p), input, *(vp(a[n]) for n in ("x", "g", "h0", "o", "hT", "saved", "ws")),
-                                 a["nbytes"], None)
+    return lib.gla_scan_fwd_save(ctypes.byref(p), input, *(vp(a[n]) for n in ("x", "g", "h0", "o", "hT", "saved")),
+                                 None)
 
 
 def scan_bwd(p, input=0, **kw):
@@ -48,15 +48,14 @@ def scan_decode(p, input=0, **kw):
 def test_scan_sizes():
     p = prob()
     assert lib.gla_scan_saved_bytes(ctypes.byref(p)) == 4 * 6 * 5 * 72           # a state every 64 tokens
-    assert lib.gla_scan_workspace_bytes(ctypes.byref(p), 0) > 0
-    assert lib.gla_scan_workspace_bytes(ctypes.byref(p), 1) >= 4 * 6 * 5 * 72    # those states
+    assert lib.gla_scan_bwd_workspace_bytes(ctypes.byref(p)) >= 4 * 6 * 5 * 72   # those states
     empty = prob(L=0)
     assert lib.gla_scan_saved_bytes(ctypes.byref(empty)) == 0
-    assert lib.gla_scan_workspace_bytes(ctypes.byref(empty), 1) > 0
+    assert lib.gla_scan_bwd_workspace_bytes(ctypes.byref(empty)) > 0
     for kw, _ in BAD_SCAN:
         q = prob(**kw)
         assert lib.gla_scan_saved_bytes(ctypes.byref(q)) == 0
-        assert lib.gla_scan_workspace_bytes(ctypes.byref(q), 0) == 0 == lib.gla_scan_workspace_bytes(ctypes.byref(q), 1)
+        assert lib.gla_scan_bwd_workspace_bytes(ctypes.byref(q)) == 0
     big = prob(B=8, H=16, L=1 << 20, D=4096)                                     # past 32 bits
     assert lib.gla_scan_saved_bytes(ctypes.byref(big)) == 4 * 128 * (1 << 14) * 4096
 
@@ -71,14 +70,14 @@ def test_scan_refuses_problems(kw, want):
 
 def test_scan_refuses_arguments():
     p = prob()
-    for call, names in ((scan_fwd, ("x", "g", "o", "ws")), (scan_bwd, ("x", "g", "dO", "dx", "dg", "ws"))):
+    for call, names in ((scan_fwd, ("x", "g", "o")), (scan_bwd, ("x", "g", "dO", "dx", "dg", "ws"))):
         for n in names:
             assert call(p, **{n: None}) == INVALID, n
         for n in names + (("h0", "hT", "saved") if call is scan_fwd else ("h0", "dhT", "saved", "dh0")):
             assert call(p, **{n: 24}) == INVALID, n
         for mode in (-1, 3):
             assert call(p, input=mode) == INVALID
-        assert call(p, nbytes=16) == WORKSPACE
+    assert scan_bwd(p, nbytes=16) == WORKSPACE
     one = prob(L=1)
     assert scan_decode(p) == INVALID                      # one token per (b, h)
     for n in ("x", "g", "state", "o"):
@@ -86,7 +85,7 @@ def test_scan_refuses_arguments():
         assert scan_decode(one, **{n: 8}) == INVALID
     assert scan_decode(one, input=7) == INVALID
     assert lib.gla_scan_decode(None, 0, None, None, None, None, None) == INVALID
-    assert lib.gla_scan_fwd(None, 0, None, None, None, None, None, None, 0, None) == INVALID
+    assert lib.gla_scan_fwd(None, 0, None, None, None, None, None, None) == INVALID
     assert lib.gla_scan_bwd(None, 0, None, None, None, None, None, None, None, None, None, 0, None) == INVALID
     assert scan_decode(prob(B=0, L=1), x=None, g=None, state=None, o=None) == _lib.GLA_OK
     assert scan_fwd(prob(H=0), x=None, g=None, o=None) == _lib.GLA_OK

@@ -271,11 +271,10 @@ def test_saved_and_recomputed_states_agree_and_repeat(L):
             assert torch.equal(a, b)
 
 
-def _call(fn, p, mode, *tensors, ws):
+def _call(fn, p, mode, *tensors, ws=()):
     from linear_rnn_b200 import _lib
     ptr = lambda t: None if t is None else ctypes.c_void_p(t.data_ptr())
-    st = fn(ctypes.byref(p), mode, *map(ptr, tensors), ptr(ws), ws.numel(),
-            ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    st = fn(ctypes.byref(p), mode, *map(ptr, tensors), *ws, ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
     assert st == _lib.GLA_OK, _lib.status_string(st)
 
 
@@ -300,18 +299,17 @@ def test_outputs_are_written_whole_and_nothing_else(size, io):
     fx, dx = buffer(x.shape, IO[io])
     fg, dg = buffer(x.shape, torch.float32)
     f0, dh0 = buffer(h0.shape, torch.float32)
-    nb = [ops.gla_scan_workspace_bytes(p, b) for b in (False, True)]
-    ws = [torch.full((n + pad,), 9, dtype=torch.uint8, device="cuda") for n in nb]
+    nb = ops.gla_scan_bwd_workspace_bytes(p)
+    ws = torch.full((nb + pad,), 9, dtype=torch.uint8, device="cuda")
     lib = _lib.lib
-    _call(lib.gla_scan_fwd_save, p, 1, x, g, h0, o, hT, sv, ws=ws[0][:nb[0]])
-    _call(lib.gla_scan_bwd_saved, p, 1, x, g, h0, dO, dhT, sv, dx, dg, dh0, ws=ws[1][:nb[1]])
+    _call(lib.gla_scan_fwd_save, p, 1, x, g, h0, o, hT, sv)
+    _call(lib.gla_scan_bwd_saved, p, 1, x, g, h0, dO, dhT, sv, dx, dg, dh0, ws=(None, 0))   # needs no workspace
     for flat in (fo, fT, fs, fx, fg, f0):
         assert torch.isfinite(flat[:-pad]).all() and (flat[-pad:] == 7).all()
     fx.fill_(float("nan")), fg.fill_(float("nan"))
-    _call(lib.gla_scan_bwd, p, 1, x, g, h0, dO, dhT, dx, dg, None, ws=ws[1][:nb[1]])
+    _call(lib.gla_scan_bwd, p, 1, x, g, h0, dO, dhT, dx, dg, None, ws=(ctypes.c_void_p(ws.data_ptr()), nb))
     assert torch.isfinite(dx).all() and torch.isfinite(dg).all()
-    for w in ws:
-        assert (w[-pad:] == 9).all()
+    assert (ws[nb:] == 9).all()
 
 
 def test_non_finite_inputs_spread_as_the_formula_says():
@@ -410,11 +408,11 @@ def test_refusals():
                 lambda: ops.gla_scan_bwd(x, g, h0, dO.float()), lambda: ops.gla_scan_bwd(x, g, h0, None),
                 lambda: ops.gla_scan_decode(x, g, h0), lambda: ops.gla_scan_fwd(x[0], g[0]),
                 lambda: ops.gla_scan_decode(x[:, :, :1].contiguous(), g[:, :, :1].contiguous(), h0[:, :1].contiguous()),
-                lambda: ops.gla_scan_fwd(x, g, workspace=torch.empty(1 << 20, dtype=torch.uint8))):
+                lambda: ops.gla_scan_bwd(x, g, h0, dO, workspace=torch.empty(1 << 20, dtype=torch.uint8))):
         with pytest.raises((ValueError, TypeError)):
             bad()
     small = torch.empty(64, dtype=torch.uint8, device="cuda")
-    for bad in (lambda: ops.gla_scan_fwd(x, g, workspace=small), lambda: ops.gla_scan_fwd(x, g, saved_states=small),
+    for bad in (lambda: ops.gla_scan_bwd(x, g, h0, dO, saved_states=small), lambda: ops.gla_scan_fwd(x, g, saved_states=small),
                 lambda: ops.gla_scan_bwd(x, g, h0, dO, workspace=small)):
         with pytest.raises(_lib.GlaError) as e:
             bad()
