@@ -266,9 +266,10 @@ gla_status gla_addnorm_fwd(const gla_norm_problem* p, const void* x, const void*
                 auto kern = k_addnorm_fwd<T, R, Sh::vec, Sh::nv, Sh::stages, decltype(kind)::value, Sh::maxt>;
                 const size_t smem = block_smem(rp, Sh::stages, thread_bytes);
                 static std::atomic<bool> seen[kMaxDevices];
+                static Occupancy known;
                 const cudaError_t e = smem_attr_once(kern, kSmSmem, seen);
                 if (e != cudaSuccess) return e;
-                const int blocks = fit_blocks(kern, rp, smem, row_blocks(rp, rows, 1), 1);
+                const int blocks = fit_blocks(kern, rp, smem, row_blocks(rp, rows, 1), 1, known);
                 GLA_LAUNCH("addnorm_fwd", st,
                            (kern<<<blocks, rp.threads, smem, st>>>(
                                static_cast<const T*>(x), static_cast<const R*>(res), rscale, w, static_cast<R*>(r),
@@ -311,9 +312,10 @@ gla_status gla_addnorm_bwd(const gla_norm_problem* p, const void* x, const void*
                     auto kern = k_addnorm_bwd<T, R, Sh::vec, Sh::nv, Sh::stages, decltype(kind)::value, Sh::maxt>;
                     const size_t smem = block_smem(rp, Sh::stages, thread_bytes);
                     static std::atomic<bool> seen[kMaxDevices];
+                static Occupancy known;
                     const cudaError_t e = smem_attr_once(kern, kSmSmem, seen);
                     if (e != cudaSuccess) return e;
-                    P = fit_blocks(kern, rp, smem, P, 1);
+                    P = fit_blocks(kern, rp, smem, P, 1, known);
                     GLA_LAUNCH("addnorm_bwd", st,
                                (kern<<<P, rp.threads, smem, st>>>(
                                    static_cast<const T*>(x), static_cast<const R*>(r), rscale, w,

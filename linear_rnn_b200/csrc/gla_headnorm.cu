@@ -319,9 +319,10 @@ gla_status gla_headnorm_fwd(const gla_norm_problem* p, const void* o, const void
                                                decltype(act)::value, Sh::maxt>;
                     const size_t smem = block_smem(rp, Sh::stages, thread_bytes);
                     static std::atomic<bool> seen[kMaxDevices];
+                static Occupancy known;
                     const cudaError_t e = smem_attr_once(kern, kSmSmem, seen);
                     if (e != cudaSuccess) return e;
-                    const dim3 grid(fit_blocks(kern, rp, smem, row_blocks(rp, tokens, p->H), p->H), p->H);
+                    const dim3 grid(fit_blocks(kern, rp, smem, row_blocks(rp, tokens, p->H), p->H, known), p->H);
                     GLA_LAUNCH("headnorm_fwd", st,
                                (kern<<<grid, rp.threads, smem, st>>>(
                                    static_cast<const T*>(o), static_cast<const T*>(z), w, static_cast<T*>(y), tokens,
@@ -361,9 +362,10 @@ gla_status gla_headnorm_bwd(const gla_norm_problem* p, const void* o, const void
                                                    decltype(act)::value, Sh::maxt>;
                         const size_t smem = block_smem(rp, Sh::stages, thread_bytes);
                         static std::atomic<bool> seen[kMaxDevices];
+                static Occupancy known;
                         const cudaError_t e = smem_attr_once(kern, kSmSmem, seen);
                         if (e != cudaSuccess) return e;
-                        P = fit_blocks(kern, rp, smem, P, p->H);
+                        P = fit_blocks(kern, rp, smem, P, p->H, known);
                         GLA_LAUNCH("headnorm_bwd", st,
                                    (kern<<<dim3(P, p->H), rp.threads, smem, st>>>(
                                        static_cast<const T*>(o), static_cast<const T*>(z), w,

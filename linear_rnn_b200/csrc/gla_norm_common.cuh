@@ -405,13 +405,23 @@ inline int row_blocks(const RowPlan& p, long long rows, int heads) {
     if (most < 1) most = 1;
     return (int)(need < most ? need : most);
 }
+// Blocks of `kern` that an SM holds, asked of the runtime once per kernel, device and block size (`known`;
+// a kernel's shared memory follows from its block size).
+using Occupancy = std::atomic<int>[kMaxDevices][33];
 template <typename K>
-int fit_blocks(K kern, const RowPlan& p, size_t smem, int blocks, int heads) {
+int fit_blocks(K kern, const RowPlan& p, size_t smem, int blocks, int heads, Occupancy& known) {
     if ((long long)blocks * heads <= tc::num_sms()) return blocks;
-    int per_sm = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, p.threads, smem) != cudaSuccess || per_sm < 1) {
-        cudaGetLastError();
-        return blocks;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return blocks;
+    std::atomic<int>& slot = known[dev][p.threads / 32];
+    int per_sm = slot.load(std::memory_order_relaxed);
+    if (per_sm == 0) {
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, p.threads, smem) != cudaSuccess ||
+            per_sm < 1) {
+            cudaGetLastError();
+            return blocks;
+        }
+        slot.store(per_sm, std::memory_order_relaxed);
     }
     const int fit = tc::num_sms() * per_sm / heads;
     return fit < 1 ? 1 : fit < blocks ? fit : blocks;

@@ -606,19 +606,38 @@ __global__ void __launch_bounds__(NT_F, 2)
     if (cs > 1) cluster_sync();
 }
 
-// One token: the state is read and written once.
+// One token: the state is read and written once. Four channels a thread; the last threads take single
+// ones.
 constexpr int NT_D = 128;
 template <typename T, int IN>
 __global__ void __launch_bounds__(NT_D) k_scan_decode(const T* __restrict__ x, const float* __restrict__ g,
                                                       float* __restrict__ state, T* __restrict__ o, size_t n) {
-    const size_t i = (size_t)blockIdx.x * NT_D + threadIdx.x;
+    const size_t i = ((size_t)blockIdx.x * NT_D + threadIdx.x) * VEC;
     if (i >= n) return;
-    uint64_t a, t, inv;
-    gate2(f2_all(g[i]), a, t);
-    float h, unused;
-    f2_split(f2_fma(a, f2_all(state[i]), times_factor2<IN>(in_factor2<IN>(t, inv), f2_all(to_f(x[i])))), h, unused);
-    state[i] = h;
-    o[i] = from_f<T>(h);
+    uint64_t xv[2], gv[2], h[2];
+    const bool whole = i + VEC <= n;
+    if (whole) {
+        ld4(x + i, xv);
+        ld4(g + i, gv);
+        ld4(state + i, h);
+    } else {
+        get4<LOAD_ONE>(x + i, xv, true, 0, (int)(n - i));
+        get4<LOAD_ONE>(g + i, gv, true, 0, (int)(n - i));
+        get4<LOAD_ONE>(state + i, h, true, 0, (int)(n - i));
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        uint64_t a, t, inv;
+        gate2(gv[k], a, t);
+        h[k] = f2_fma(a, h[k], times_factor2<IN>(in_factor2<IN>(t, inv), xv[k]));
+    }
+    if (whole) {
+        st4(state + i, h);
+        st4(o + i, h);
+    } else {
+        put4<LOAD_ONE>(state + i, h, 0, (int)(n - i));
+        put4<LOAD_ONE>(o + i, h, 0, (int)(n - i));
+    }
 }
 
 // Calls f(T{}, integral_constant<IN>) for the problem's dtype and input factor.
@@ -834,7 +853,7 @@ gla_status gla_scan_decode(const gla_problem* p, int input, const void* x, const
     cudaStream_t st = (cudaStream_t)stream;
     const cudaError_t e = dispatch(p, input, [&](auto tv, auto in) {
         using T = decltype(tv);
-        const size_t blocks = (n + NT_D - 1) / NT_D;
+        const size_t blocks = (n + NT_D * VEC - 1) / (NT_D * VEC);
         if (blocks > 2147483647u) return cudaErrorInvalidConfiguration;
         GLA_LAUNCH("scan_decode", st,
                    (k_scan_decode<T, decltype(in)::value><<<(unsigned)blocks, NT_D, 0, st>>>(
