@@ -21,7 +21,7 @@ __global__ void __launch_bounds__(MAXT, 1024 / MAXT)   // 64 registers: 4 blocks
     constexpr int XOFF = F::template bytes<R, VEC, NV>();   // res first, then x
     constexpr int ROW = XOFF + F::template bytes<T, VEC, NV>();
     RowSum sum{reinterpret_cast<float*>(smem), G, 0};
-    F feed{smem + kHead + 16 * threadIdx.x, ROW * (int)blockDim.x, 0, 0};
+    F feed{smem + kHead + 16 * threadIdx.x, ROW * (int)blockDim.x, 0};
     const int grp = threadIdx.x / G, ngrp = blockDim.x / G;
     const Place P{(int)threadIdx.x - grp * G, G, D / VEC};
     const float inv_d = 1.f / D;
@@ -31,7 +31,7 @@ __global__ void __launch_bounds__(MAXT, 1024 / MAXT)   // 64 registers: 4 blocks
     const long long step = (long long)gridDim.x * ngrp;
     long long row = (long long)blockIdx.x * ngrp + grp;
     auto copy = [&](long long to, int stage) {
-        if (S > 0) {
+        if constexpr (S > 0) {
             if (to < rows)
 #pragma unroll
                 for (int j = 0; j < NV; ++j)
@@ -45,6 +45,18 @@ __global__ void __launch_bounds__(MAXT, 1024 / MAXT)   // 64 registers: 4 blocks
     };
 #pragma unroll
     for (int k = 0; k + 1 < S; ++k) copy(row + k * step, k);
+    uint64_t xn[NV][NP] = {}, rn[NV][NP] = {};
+    auto hold = [&](long long to) {
+        if (kHold<S, NV> && to < rows)
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+                if (P.has(j)) {
+                    const size_t c = (size_t)to * D + P.col<VEC>(j);
+                    load_piece<VEC>(x + c, xn[j]);
+                    if (res) load_piece<VEC>(res + c, rn[j]);
+                }
+    };
+    hold(row);
     // every group of a block takes as many turns: the row sums are the block's business
     for (long long first = (long long)blockIdx.x * ngrp; first < rows; first += step, row += step) {
         const bool live = row < rows;
@@ -63,6 +75,9 @@ __global__ void __launch_bounds__(MAXT, 1024 / MAXT)   // 64 registers: 4 blocks
                 if constexpr (S > 0) {
                     feed.template read<T, VEC>(XOFF, j, xv);
                     if (res) feed.template read<R, VEC>(0, j, r[j]);
+                } else if constexpr (kHold<S, NV>) {
+#pragma unroll
+                    for (int i = 0; i < NP; ++i) xv[i] = xn[j][i], r[j][i] = rn[j][i];
                 } else {
                     load_piece<VEC>(x + off + P.col<VEC>(j), xv);
                     if (res) load_piece<VEC>(res + off + P.col<VEC>(j), r[j]);
@@ -72,6 +87,7 @@ __global__ void __launch_bounds__(MAXT, 1024 / MAXT)   // 64 registers: 4 blocks
                 if (r_out) store_piece<VEC>(r_out + off + P.col<VEC>(j), r[j]);
             }
         }
+        hold(row + step);
         center<KIND, VEC, NV>(sum, r, P, inv_d);
         float s[1] = {square_sum<VEC, NV>(r)};
         sum(s);
@@ -98,7 +114,7 @@ __global__ void __launch_bounds__(MAXT)
     constexpr int BR = F::template bytes<R, VEC, NV>(), BT = F::template bytes<T, VEC, NV>();
     constexpr int DROFF = BR, DYOFF = 2 * BR, XOFF = 2 * BR + BT, ROW = 2 * (BR + BT);   // r, dr, dy, x
     RowSum sum{reinterpret_cast<float*>(smem), G, 0};
-    F feed{smem + kHead + 16 * threadIdx.x, ROW * (int)blockDim.x, 0, 0};
+    F feed{smem + kHead + 16 * threadIdx.x, ROW * (int)blockDim.x, 0};
     const int grp = threadIdx.x / G, ngrp = blockDim.x / G;
     const Place P{(int)threadIdx.x - grp * G, G, D / VEC};
     const float inv_d = 1.f / D;
@@ -108,7 +124,7 @@ __global__ void __launch_bounds__(MAXT)
     const long long step = (long long)gridDim.x * ngrp;
     long long row = (long long)blockIdx.x * ngrp + grp;
     auto copy = [&](long long to, int stage) {
-        if (S > 0) {
+        if constexpr (S > 0) {
             if (to < rows)
 #pragma unroll
                 for (int j = 0; j < NV; ++j)
@@ -124,6 +140,20 @@ __global__ void __launch_bounds__(MAXT)
     };
 #pragma unroll
     for (int k = 0; k + 1 < S; ++k) copy(row + k * step, k);
+    uint64_t rn[NV][NP] = {}, dn[NV][NP] = {}, drn[NV][NP] = {}, xn[NV][NP] = {};
+    auto hold = [&](long long to) {
+        if (kHold<S, NV> && to < rows)
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+                if (P.has(j)) {
+                    const size_t c = (size_t)to * D + P.col<VEC>(j);
+                    load_piece<VEC>(r_in + c, rn[j]);
+                    load_piece<VEC>(dy + c, dn[j]);
+                    if (dr) load_piece<VEC>(dr + c, drn[j]);
+                    if (pds) load_piece<VEC>(x + c, xn[j]);
+                }
+    };
+    hold(row);
     for (long long first = (long long)blockIdx.x * ngrp; first < rows; first += step, row += step) {
         const bool live = row < rows;
         const size_t off = (size_t)row * D;
@@ -132,20 +162,28 @@ __global__ void __launch_bounds__(MAXT)
             copy(row + (S - 1) * step, feed.ahead());
         }
         uint64_t r[NV][NP], d[NV][NP];   // r - mu, then n; dy, then d = dy w
+        uint64_t drc[NV][NP], xc[NV][NP];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
+            if (kHold<S, NV>)
+#pragma unroll
+                for (int i = 0; i < NP; ++i) drc[j][i] = drn[j][i], xc[j][i] = xn[j][i];
 #pragma unroll
             for (int i = 0; i < NP; ++i) r[j][i] = d[j][i] = 0;
             if (live && P.has(j)) {
                 if constexpr (S > 0) {
                     feed.template read<R, VEC>(0, j, r[j]);
                     feed.template read<T, VEC>(DYOFF, j, d[j]);
+                } else if constexpr (kHold<S, NV>) {
+#pragma unroll
+                    for (int i = 0; i < NP; ++i) r[j][i] = rn[j][i], d[j][i] = dn[j][i];
                 } else {
                     load_piece<VEC>(r_in + off + P.col<VEC>(j), r[j]);
                     load_piece<VEC>(dy + off + P.col<VEC>(j), d[j]);
                 }
             }
         }
+        hold(row + step);
         center<KIND, VEC, NV>(sum, r, P, inv_d);
         // sums of (r - mu)^2, d (r - mu) and, for the layer norm, d
         uint64_t t0 = 0, t1 = 0, t2 = 0;
@@ -175,8 +213,14 @@ __global__ void __launch_bounds__(MAXT)
 #pragma unroll
                 for (int i = 0; i < NP; ++i) t[i] = 0;
                 if (dr) {
-                    if constexpr (S > 0) feed.template read<R, VEC>(DROFF, j, t);
-                    else load_piece<VEC>(dr + off + P.col<VEC>(j), t);
+                    if constexpr (S > 0) {
+                        feed.template read<R, VEC>(DROFF, j, t);
+                    } else if constexpr (kHold<S, NV>) {
+#pragma unroll
+                        for (int i = 0; i < NP; ++i) t[i] = drc[j][i];
+                    } else {
+                        load_piece<VEC>(dr + off + P.col<VEC>(j), t);
+                    }
                 }
 #pragma unroll
                 for (int i = 0; i < NP; ++i) {
@@ -188,8 +232,14 @@ __global__ void __launch_bounds__(MAXT)
                 }
                 if (dres) store_piece<VEC>(dres + off + P.col<VEC>(j), t);
                 if (pds) {
-                    if constexpr (S > 0) feed.template read<T, VEC>(XOFF, j, xv);
-                    else load_piece<VEC>(x + off + P.col<VEC>(j), xv);
+                    if constexpr (S > 0) {
+                        feed.template read<T, VEC>(XOFF, j, xv);
+                    } else if constexpr (kHold<S, NV>) {
+#pragma unroll
+                        for (int i = 0; i < NP; ++i) xv[i] = xc[j][i];
+                    } else {
+                        load_piece<VEC>(x + off + P.col<VEC>(j), xv);
+                    }
 #pragma unroll
                     for (int i = 0; i < NP; ++i) as[j][i] = f2_fma(t[i], xv[i], as[j][i]);
                 }
@@ -219,7 +269,9 @@ cudaError_t by_dtypes(gla_dtype io, gla_dtype res, F&& f) {
     return res == GLA_F32 ? f(__nv_bfloat16{}, float{}) : f(__nv_bfloat16{}, __nv_bfloat16{});
 }
 
-RowPlan plan(const gla_norm_problem* p) { return row_plan(p->D, p->io == GLA_BF16 && p->res == GLA_BF16); }
+RowPlan plan(const gla_norm_problem* p) {
+    return row_plan(p->D, p->io == GLA_BF16 && p->res == GLA_BF16, p->io == GLA_F32);
+}
 
 gla_status check(const gla_norm_problem* p) {
     const gla_status s = check_common(p);
@@ -259,8 +311,7 @@ gla_status gla_addnorm_fwd(const gla_norm_problem* p, const void* x, const void*
         using R = decltype(rv);
         const int thread_bytes = rp.nv * rp.vec * (int)(sizeof(T) + sizeof(R));
         const int stages = ring_stages(rp, thread_bytes);
-        return by_shape<std::is_same<T, __nv_bfloat16>::value && std::is_same<R, __nv_bfloat16>::value>(
-            rp, stages, [&](auto sh) {
+        return by_shape<sizeof(T) + sizeof(R) == 4, sizeof(T) == 4>(rp, stages, [&](auto sh) {
             return by_kind(p->kind, [&](auto kind) {
                 using Sh = decltype(sh);
                 auto kern = k_addnorm_fwd<T, R, Sh::vec, Sh::nv, Sh::stages, decltype(kind)::value, Sh::maxt>;
@@ -305,8 +356,7 @@ gla_status gla_addnorm_bwd(const gla_norm_problem* p, const void* x, const void*
             using R = decltype(rv);
             const int thread_bytes = 2 * rp.nv * rp.vec * (int)(sizeof(T) + sizeof(R));
             const int stages = ring_stages(rp, thread_bytes);
-            return by_shape<std::is_same<T, __nv_bfloat16>::value && std::is_same<R, __nv_bfloat16>::value>(
-            rp, stages, [&](auto sh) {
+            return by_shape<sizeof(T) + sizeof(R) == 4, sizeof(T) == 4>(rp, stages, [&](auto sh) {
                 return by_kind(p->kind, [&](auto kind) {
                     using Sh = decltype(sh);
                     auto kern = k_addnorm_bwd<T, R, Sh::vec, Sh::nv, Sh::stages, decltype(kind)::value, Sh::maxt>;

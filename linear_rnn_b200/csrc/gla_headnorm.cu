@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(MAXT)
     using F = Feed<S>;
     constexpr int ZOFF = F::template bytes<T, VEC, NV>(), ROW = 2 * ZOFF;
     RowSum sum{reinterpret_cast<float*>(smem), G, 0};
-    F feed{smem + kHead + 16 * threadIdx.x, ROW * (int)blockDim.x, 0, 0};
+    F feed{smem + kHead + 16 * threadIdx.x, ROW * (int)blockDim.x, 0};
     const int grp = threadIdx.x / G, ngrp = blockDim.x / G, h = blockIdx.y;
     const Place P{(int)threadIdx.x - grp * G, G, D / VEC};
     const float inv_d = 1.f / D;
@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(MAXT)
     const Walk walk(step, H, L, D);
     Token in = walk.first(t, h, H, D), out = in;   // the next token to copy, the current one
     auto copy = [&](int stage) {
-        if (S > 0) {
+        if constexpr (S > 0) {
             if (ahead < tokens)
 #pragma unroll
                 for (int j = 0; j < NV; ++j)
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(MAXT)
     using F = Feed<S>;
     constexpr int ZOFF = F::template bytes<T, VEC, NV>(), YOFF = 2 * ZOFF, ROW = 3 * ZOFF;
     RowSum sum{reinterpret_cast<float*>(smem), G, 0};
-    F feed{smem + kHead + 16 * threadIdx.x, ROW * (int)blockDim.x, 0, 0};
+    F feed{smem + kHead + 16 * threadIdx.x, ROW * (int)blockDim.x, 0};
     const int grp = threadIdx.x / G, ngrp = blockDim.x / G, h = blockIdx.y;
     const Place P{(int)threadIdx.x - grp * G, G, D / VEC};
     const float inv_d = 1.f / D;
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(MAXT)
     const Walk walk(step, H, L, D);
     Token in = walk.first(t, h, H, D), out = in;   // the next token to copy, the current one
     auto copy = [&](int stage) {
-        if (S > 0) {
+        if constexpr (S > 0) {
             if (ahead < tokens)
 #pragma unroll
                 for (int j = 0; j < NV; ++j)
@@ -293,7 +293,7 @@ extern "C" {
 
 size_t gla_headnorm_workspace_bytes(const gla_norm_problem* p) {
     if (check(p) != GLA_OK) return 0;
-    const int P = p->H ? row_blocks(row_plan(p->D, p->io == GLA_BF16), (long long)p->B * p->L, p->H) : 0;
+    const int P = p->H ? row_blocks(row_plan(p->D, p->io == GLA_BF16, p->io == GLA_F32), (long long)p->B * p->L, p->H) : 0;
     return 256 + (size_t)P * p->H * p->D * 4;
 }
 
@@ -307,11 +307,11 @@ gla_status gla_headnorm_fwd(const gla_norm_problem* p, const void* o, const void
     if (tokens == 0 || p->H == 0) return GLA_OK;
     if (!o || !y) return GLA_ERR_INVALID_ARG;
     cudaStream_t st = (cudaStream_t)stream;
-    const RowPlan rp = row_plan(p->D, p->io == GLA_BF16);
+    const RowPlan rp = row_plan(p->D, p->io == GLA_BF16, p->io == GLA_F32);
     const cudaError_t e = by_io(p->io, [&](auto tv) {
         using T = decltype(tv);
         const int thread_bytes = 2 * rp.nv * rp.vec * (int)sizeof(T);
-        return by_shape<std::is_same<T, __nv_bfloat16>::value>(rp, ring_stages(rp, thread_bytes), [&](auto sh) {
+        return by_shape<sizeof(T) == 2, sizeof(T) == 4>(rp, ring_stages(rp, thread_bytes), [&](auto sh) {
             return by_kind(p->kind, [&](auto kind) {
                 return by_act(p->act, [&](auto act) {
                     using Sh = decltype(sh);
@@ -345,7 +345,7 @@ gla_status gla_headnorm_bwd(const gla_norm_problem* p, const void* o, const void
     cudaStream_t st = (cudaStream_t)stream;
     const int tokens = p->B * p->L;
     if (p->H == 0 && (!dw || p->w_per_head)) return GLA_OK;
-    const RowPlan rp = row_plan(p->D, p->io == GLA_BF16);
+    const RowPlan rp = row_plan(p->D, p->io == GLA_BF16, p->io == GLA_F32);
     int P = p->H ? row_blocks(rp, tokens, p->H) : 0;
     float* pdw = dw ? static_cast<float*>(ws) : nullptr;
     cudaError_t e = cudaSuccess;
@@ -354,7 +354,7 @@ gla_status gla_headnorm_bwd(const gla_norm_problem* p, const void* o, const void
         e = by_io(p->io, [&](auto tv) {
             using T = decltype(tv);
             const int thread_bytes = 3 * rp.nv * rp.vec * (int)sizeof(T);
-            return by_shape<std::is_same<T, __nv_bfloat16>::value>(rp, ring_stages(rp, thread_bytes), [&](auto sh) {
+            return by_shape<sizeof(T) == 2, sizeof(T) == 4>(rp, ring_stages(rp, thread_bytes), [&](auto sh) {
                 return by_kind(p->kind, [&](auto kind) {
                     return by_act(p->act, [&](auto act) {
                         using Sh = decltype(sh);

@@ -51,6 +51,8 @@ template <int VEC>
 __device__ __forceinline__ void load_piece(const float* p, uint64_t (&v)[kPairs<VEC>]) {
     if constexpr (VEC == 1) {
         v[0] = f2(*p, 0.f);
+    } else if constexpr (VEC == 2) {
+        v[0] = *reinterpret_cast<const uint64_t*>(p);
     } else {
 #pragma unroll
         for (int i = 0; i < VEC / 4; ++i) {
@@ -66,7 +68,9 @@ __device__ __forceinline__ void load_piece(const __nv_bfloat16* p, uint64_t (&v)
         v[0] = f2(__bfloat162float(*p), 0.f);
     } else {
         uint32_t w[VEC / 2];
-        if constexpr (VEC == 8) {
+        if constexpr (VEC == 2) {
+            w[0] = *reinterpret_cast<const uint32_t*>(p);
+        } else if constexpr (VEC == 8) {
             const uint4 u = *reinterpret_cast<const uint4*>(p);
             w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
         } else {
@@ -83,6 +87,8 @@ __device__ __forceinline__ void store_piece(float* p, const uint64_t (&v)[kPairs
         float a, b;
         f2_split(v[0], a, b);
         *p = a;
+    } else if constexpr (VEC == 2) {
+        *reinterpret_cast<uint64_t*>(p) = v[0];
     } else {
 #pragma unroll
         for (int i = 0; i < VEC / 4; ++i)
@@ -101,6 +107,8 @@ __device__ __forceinline__ void store_piece(__nv_bfloat16* p, const uint64_t (&v
         float a, b;
         f2_split(v[0], a, b);
         *p = __float2bfloat16_rn(a);
+    } else if constexpr (VEC == 2) {
+        *reinterpret_cast<uint32_t*>(p) = to_bf16x2(v[0]);
     } else if constexpr (VEC == 8) {
         *reinterpret_cast<uint4*>(p) =
             make_uint4(to_bf16x2(v[0]), to_bf16x2(v[1]), to_bf16x2(v[2]), to_bf16x2(v[3]));
@@ -118,14 +126,14 @@ struct Place {
 };
 
 // ------------------------------------------------------------------ the ring
-// S stages of shared memory that belong to the thread alone: piece j of input `in` of a stage lies, in units of
-// 16 bytes (8 for bf16 pieces of four), blockDim units apart from the next, so a warp's accesses
-// are contiguous. Stages are written by cp.async, one commit group per row; wait() leaves the groups of
-// the S - 1 rows that follow in flight.
+// S stages of shared memory that belong to the thread alone. Piece j of an input lies in units of up to 16 bytes,
+// blockDim units of that size apart from the next piece, so that a warp's accesses are contiguous.
+// Stages are written by cp.async, one commit group per row; wait() leaves the groups of the S - 1 rows that
+// follow in flight.
 template <int S>
 struct Feed {
-    uint8_t* mine;      // this thread's first byte, in the first stage
-    int stage_bytes, unit_stride;
+    uint8_t* mine;      // first stage, 16 bytes per thread on
+    int stage_bytes;
     int s;              // stage of the current row
 
     // Room of one input's NV pieces, in bytes per thread.
@@ -134,8 +142,9 @@ struct Feed {
 
     template <typename T, int VEC>
     __device__ __forceinline__ uint8_t* at(int stage, int thread_off, int j) const {
-        constexpr int B = VEC * (int)sizeof(T);
-        return mine + stage * stage_bytes + (thread_off + j * B) * (int)blockDim.x;
+        constexpr int B = VEC * (int)sizeof(T), U = B < 16 ? B : 16;
+        uint8_t* d = mine + stage * stage_bytes + (thread_off + j * B) * (int)blockDim.x;
+        return U == 16 ? d : d - (16 - U) * (int)threadIdx.x;
     }
     template <typename T, int VEC>
     __device__ __forceinline__ void copy(int stage, int thread_off, int j, const T* src) const {
@@ -148,9 +157,8 @@ struct Feed {
                              "l"(reinterpret_cast<const uint8_t*>(src) + 16 * u)
                              : "memory");
         } else {
-            // threads of 8-byte pieces share 16-byte units
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(d - 8 * (int)threadIdx.x)), "l"(src)
-                         : "memory");
+            static_assert(B == 4 || B == 8, "");
+            asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(d)), "l"(src), "n"(B) : "memory");
         }
     }
     template <typename T, int VEC>
@@ -162,10 +170,8 @@ struct Feed {
             load_piece<4>(reinterpret_cast<const float*>(d), a);
             load_piece<4>(reinterpret_cast<const float*>(d + 16 * (int)blockDim.x), b);
             v[0] = a[0]; v[1] = a[1]; v[2] = b[0]; v[3] = b[1];
-        } else if constexpr (B == 16) {
-            load_piece<VEC>(reinterpret_cast<const T*>(d), v);
         } else {
-            load_piece<VEC>(reinterpret_cast<const T*>(d - 8 * (int)threadIdx.x), v);
+            load_piece<VEC>(reinterpret_cast<const T*>(d), v);
         }
     }
     __device__ __forceinline__ void commit() const { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -175,6 +181,10 @@ struct Feed {
     __device__ __forceinline__ int ahead() const { return s == 0 ? S - 1 : s - 1; }   // stage of the row S - 1 ahead
     __device__ __forceinline__ void next() { s = s + 1 == S ? 0 : s + 1; }
 };
+
+// Without a ring (odd rows of bf16): whether the next row's pieces wait in registers instead.
+template <int S, int NV>
+constexpr bool kHold = S == 0 && NV <= 4;
 
 // ------------------------------------------------------------------ sums over a row
 // Sums of K <= 4 values over the G threads of a row; every thread of the block calls. G < 32: plain
@@ -353,19 +363,19 @@ inline cudaError_t colsum(const float* part0, float* out0, const float* part1, f
 // ------------------------------------------------------------------ host side
 // Threads and pieces of a row. A piece is 16 bytes of the widest type in the row (8 bf16, or 4 where
 // fp32 stands beside them: with 8 the fp32 accesses of a warp would leave every other 16 bytes out,
-// 305 instead of 224 us for the backward of 16384 x 4096 with an fp32 residual), 4 elements where D is
-// no multiple of 8, one where it is no multiple of 4. A thread holds 16 elements, so that the row sums'
-// exchange and the addresses of a row are spread over many (4 for single elements up to D = 2048); a
-// row has a power of two of lanes up to a warp (D <= 512), whole warps beyond.
+// 305 instead of 212 us for the backward of 16384 x 4096 with an fp32 residual), 4 elements where D is no
+// multiple of 8, then 2, then 1. A thread holds 16 elements, so that the row sums' exchange and the
+// addresses of a row are spread over many; with narrower pieces 4 of them while 512 threads do. A row has a
+// power of two of lanes up to a warp, whole warps beyond.
 struct RowPlan {
     int vec, nv, G, threads;
-    bool big;   // more than 512 threads: D > 8192
+    bool ring;   // pieces of 4 bytes or more in every operand, at most 512 threads
 };
-inline RowPlan row_plan(int D, bool all_bf16) {
+inline RowPlan row_plan(int D, bool all_bf16, bool all_f32) {
     RowPlan p;
-    p.vec = all_bf16 && D % 8 == 0 ? 8 : D % 4 == 0 ? 4 : 1;
+    p.vec = all_bf16 && D % 8 == 0 ? 8 : D % 4 == 0 ? 4 : D % 2 == 0 ? 2 : 1;
     const int nvec = D / p.vec;
-    p.nv = p.vec == 1 && D <= 2048 ? 4 : 16 / p.vec;
+    p.nv = p.vec < 4 && nvec <= 2048 ? 4 : 16 / p.vec;
     const int need = cdiv(nvec, p.nv);
     if (need > 32) {
         p.G = cdiv(need, 32) * 32;
@@ -374,18 +384,17 @@ inline RowPlan row_plan(int D, bool all_bf16) {
         for (p.G = 1; p.G < need;) p.G *= 2;
         p.threads = 256;
     }
-    p.big = p.threads > 512;
+    p.ring = p.threads <= 512 && (p.vec > 1 || all_f32) && !(p.vec < 4 && p.nv > 4);
     return p;
 }
 // Shared memory in front of the ring: the row sums' buffer; it and the ring are free again when the column
 // sums of a block's row groups need their blockDim * 16 floats at most.
 constexpr int kHead = 1024;
 constexpr int kSmSmem = 220 * 1024;    // of an SM, for its blocks
-// Stages of the ring: 3 where two blocks of them fit an SM, else 2 where one does, else none (as for pieces of
-// one element).
+// Stages of the ring: 3 where two blocks of them fit an SM, else 2 where one does, else none.
 inline int ring_stages(const RowPlan& p, int thread_bytes) {
     const int row = thread_bytes * p.threads;
-    if (p.vec == 1 || p.big) return 0;
+    if (!p.ring) return 0;
     if (2 * (3 * row + kHead + 1024) <= kSmSmem) return 3;
     return 2 * row + kHead + 1024 <= kSmSmem ? 2 : 0;
 }
@@ -431,23 +440,28 @@ int fit_blocks(K kern, const RowPlan& p, size_t smem, int blocks, int heads, Occ
 template <int V, int N, int S, int M> struct Shape {
     static constexpr int vec = V, nv = N, stages = S, maxt = M;
 };
-// BF16: every operand of the row is bf16, so pieces of 8 exist too.
-template <bool BF16, typename F>
+// BF16, F32: every operand of the row has that type, so pieces of 8, and a ring of single elements, exist too.
+// Without a ring up to 1024 threads: with 16 elements each they spill; only rows beyond 8192 elements.
+template <bool BF16, bool F32, typename F>
 cudaError_t by_shape(const RowPlan& p, int stages, F&& f) {
-    constexpr int W = BF16 ? 8 : 4;
     if (p.vec == 1) {
-        if (p.big) return f(Shape<1, 16, 0, 1024>{});
-        return p.nv == 4 ? f(Shape<1, 4, 0, 512>{}) : f(Shape<1, 16, 0, 512>{});
+        if (p.nv == 16) return f(Shape<1, 16, 0, 1024>{});
+        if constexpr (F32)
+            if (stages == 3) return f(Shape<1, 4, 3, 512>{});
+        return f(Shape<1, 4, 0, 512>{});
     }
-    if (p.vec == W) {
-        if (stages == 0) return f(Shape<W, 16 / W, 0, 1024>{});
-        return stages == 3 ? f(Shape<W, 16 / W, 3, 512>{}) : f(Shape<W, 16 / W, 2, 512>{});
+    if (p.vec == 2) {
+        if (p.nv == 8) return f(Shape<2, 8, 0, 1024>{});
+        return stages == 3 ? f(Shape<2, 4, 3, 512>{}) : f(Shape<2, 4, 0, 512>{});
     }
-    if constexpr (W == 8) {   // D a multiple of 4 only
-        if (stages == 0) return f(Shape<4, 4, 0, 1024>{});
-        return stages == 3 ? f(Shape<4, 4, 3, 512>{}) : f(Shape<4, 4, 2, 512>{});
-    }
-    return cudaErrorInvalidValue;
+    if constexpr (BF16)
+        if (p.vec == 8)
+            return stages == 3   ? f(Shape<8, 2, 3, 512>{})
+                   : stages == 2 ? f(Shape<8, 2, 2, 512>{})
+                                 : f(Shape<8, 2, 0, 1024>{});
+    return stages == 3   ? f(Shape<4, 4, 3, 512>{})
+           : stages == 2 ? f(Shape<4, 4, 2, 512>{})
+                         : f(Shape<4, 4, 0, 1024>{});
 }
 template <typename F>
 cudaError_t by_kind(int kind, F&& f) {

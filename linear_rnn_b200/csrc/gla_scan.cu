@@ -35,11 +35,13 @@ constexpr int RW = 32 / CHL;     // runs of a warp
 constexpr int WT = RW * RUN;     // tokens of a warp
 constexpr int TT = NW * WT;      // tokens of a tile
 constexpr int ELEMS = TT * CH;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;  // above 8 only with the attribute for it
 constexpr int kFwdStages = 3;    // tiles of the forward's ring
 
-// How a tile reaches shared memory.
-enum { LOAD_TMA = 0, LOAD_VEC4 = 1, LOAD_ONE = 2 };
+// How a tile reaches shared memory: whole boxes by TMA, or each thread's own four channels by cp.async, in pieces of
+// four, two or one channel(s) as D allows. bf16 pieces of one channel (odd D) are narrower than cp.async's
+// 4 bytes: plain loads and shared stores.
+enum { LOAD_TMA = 0, LOAD_4 = 4, LOAD_2 = 2, LOAD_1 = 1 };
 
 // ------------------------------------------------------------------ packed pairs of fp32
 using tc::f2;
@@ -138,27 +140,49 @@ __device__ __forceinline__ uint32_t to_bf16x2(uint64_t v) {
 __device__ __forceinline__ void st4(__nv_bfloat16* p, const uint64_t (&v)[2]) {
     *reinterpret_cast<uint2*>(p) = make_uint2(to_bf16x2(v[0]), to_bf16x2(v[1]));
 }
-// Stores the channels c .. c+3 that exist; whole vectors where D allows.
-template <int LOAD, typename T>
-__device__ __forceinline__ void put4(T* p, const uint64_t (&v)[2], int c, int D) {
-    if (LOAD != LOAD_ONE) {
+// Stores the channels c .. c+3 that exist, in pieces of PIECE (D is a multiple of it; p too is aligned to it).
+template <int PIECE>
+__device__ __forceinline__ void put4(float* p, const uint64_t (&v)[2], int c, int D) {
+    if (PIECE == 4) {
         if (c < D) st4(p, v);
     } else {
-        float f[VEC];
-        f2_split(v[0], f[0], f[1]);
-        f2_split(v[1], f[2], f[3]);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i)
-            if (c + i < D) p[i] = from_f<T>(f[i]);
+        for (int k = 0; k < 2; ++k) {
+            float lo, hi;
+            f2_split(v[k], lo, hi);
+            if (PIECE == 2) {
+                if (c + 2 * k < D) *reinterpret_cast<float2*>(p + 2 * k) = make_float2(lo, hi);
+            } else {
+                if (c + 2 * k < D) p[2 * k] = lo;
+                if (c + 2 * k + 1 < D) p[2 * k + 1] = hi;
+            }
+        }
     }
 }
-
+template <int PIECE>
+__device__ __forceinline__ void put4(__nv_bfloat16* p, const uint64_t (&v)[2], int c, int D) {
+    if (PIECE == 4) {
+        if (c < D) st4(p, v);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if (PIECE == 2) {
+                if (c + 2 * k < D) *reinterpret_cast<uint32_t*>(p + 2 * k) = to_bf16x2(v[k]);
+            } else {
+                float lo, hi;
+                f2_split(v[k], lo, hi);
+                if (c + 2 * k < D) p[2 * k] = __float2bfloat16_rn(lo);
+                if (c + 2 * k + 1 < D) p[2 * k + 1] = __float2bfloat16_rn(hi);
+            }
+        }
+    }
+}
 // Loads them the same way, zeros (the identity: a = 1, b = 0) where there are none.
-template <int LOAD, typename T>
+template <int PIECE, typename T>
 __device__ __forceinline__ void get4(const T* p, uint64_t (&v)[2], bool row, int c, int D) {
     v[0] = v[1] = 0;
     if (!row) return;
-    if (LOAD != LOAD_ONE) {
+    if (PIECE == 4) {
         if (c < D) ld4(p, v);
     } else {
         float f[VEC];
@@ -167,6 +191,33 @@ __device__ __forceinline__ void get4(const T* p, uint64_t (&v)[2], bool row, int
         v[0] = f2(f[0], f[1]);
         v[1] = f2(f[2], f[3]);
     }
+}
+// Copies them to shared memory, asynchronously where a piece has 4 bytes or more; zeros where there are none.
+template <int PIECE, typename T>
+__device__ __forceinline__ void fetch4(T* dst, const T* src, bool row, int c, int D) {
+    constexpr int B = PIECE * (int)sizeof(T);
+    if constexpr (B >= 4) {
+#pragma unroll
+        for (int i = 0; i < VEC; i += PIECE) {
+            const int n = row && c + i < D ? B : 0;   // bytes read; the rest is filled with zeros
+            if constexpr (B == 16)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst + i)), "l"(src + (n ? i : 0)),
+                             "r"(n)
+                             : "memory");
+            else
+                asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(dst + i)), "l"(src + (n ? i : 0)),
+                             "n"(B), "r"(n)
+                             : "memory");
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) dst[i] = row && c + i < D ? src[i] : from_f<T>(0.f);
+    }
+}
+__device__ __forceinline__ void fetch_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void fetch_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // A pair into shared memory of a CTA of the cluster, counted on that CTA's barrier.
@@ -246,7 +297,8 @@ __global__ void __launch_bounds__(NT_F, 2)
                int cs) {
     extern __shared__ __align__(128) uint8_t smem[];
     constexpr int kStage = ELEMS * (4 + (int)sizeof(T));
-    FwdTail& sm = *reinterpret_cast<FwdTail*>(smem + (LOAD == LOAD_TMA ? kFwdStages * kStage : 0));
+    constexpr int PIECE = LOAD == LOAD_TMA ? 4 : LOAD;
+    FwdTail& sm = *reinterpret_cast<FwdTail*>(smem + kFwdStages * kStage);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = cs > 1 ? (int)cluster_rank() : 0;
     const unsigned chain = blockIdx.x / cs;
@@ -276,23 +328,40 @@ __global__ void __launch_bounds__(NT_F, 2)
         const float* gg = P.g + bh * L * D + c0 + ch;
         T* og = static_cast<T*>(P.out) + bh * L * D + c0 + ch;
 
+        auto fetch = [&](int i) {   // this thread's part of tile i, without TMA
+            if (i < P.steps) {
+                const int s = i % kFwdStages, t = (i * cs + rank) * TT + tr;
+                float* sg = reinterpret_cast<float*>(smem + s * kStage) + tr * CH + ch;
+                T* sx = reinterpret_cast<T*>(smem + s * kStage + ELEMS * 4) + tr * CH + ch;
+#pragma unroll
+                for (int j = 0; j < RUN; ++j) {
+                    const size_t at = (size_t)(t + j) * D;
+                    const bool row = t + j < L && c0 + ch < D;
+                    fetch4<PIECE>(sg + j * CH, row ? gg + at : P.g, row, c0 + ch, D);
+                    fetch4<PIECE>(sx + j * CH, row ? xg + at : static_cast<const T*>(P.x), row, c0 + ch, D);
+                }
+            }
+            fetch_commit();
+        };
+        if (LOAD != LOAD_TMA)
+            for (int i = 0; i + 1 < kFwdStages; ++i) fetch(i);
         auto compose = [&](int i, uint64_t (&a)[RUN][2], uint64_t (&b)[RUN][2], uint64_t (&A)[2], uint64_t (&B)[2]) {
             const int s = i % kFwdStages;
             const float* sg = reinterpret_cast<const float*>(smem + s * kStage) + tr * CH + ch;
             const T* sx = reinterpret_cast<const T*>(smem + s * kStage + ELEMS * 4) + tr * CH + ch;
-            const int t = (i * cs + rank) * TT + tr;
-            if (LOAD == LOAD_TMA && ok) ok = mbar_wait(&sm.full[s], (i / kFwdStages) & 1);
+            if (LOAD == LOAD_TMA) {
+                if (ok) ok = mbar_wait(&sm.full[s], (i / kFwdStages) & 1);
+            } else {
+                fetch_wait<kFwdStages - 2>();
+            }
             uint64_t gv[RUN][2], xv[RUN][2];
 #pragma unroll
             for (int j = 0; j < RUN; ++j) {
-                if (LOAD == LOAD_TMA) {
-                    ld4(sg + j * CH, gv[j]);
-                    ld4(sx + j * CH, xv[j]);
-                } else {
-                    get4<LOAD>(gg + (size_t)(t + j) * D, gv[j], t + j < L, c0 + ch, D);
-                    get4<LOAD>(xg + (size_t)(t + j) * D, xv[j], t + j < L, c0 + ch, D);
-                }
+                ld4(sg + j * CH, gv[j]);
+                ld4(sx + j * CH, xv[j]);
             }
+            // the stage of tile i - 1, which this thread has read
+            if (LOAD != LOAD_TMA) fetch(i + kFwdStages - 1);
 #pragma unroll
             for (int j = 0; j < RUN; ++j)
 #pragma unroll
@@ -325,7 +394,7 @@ __global__ void __launch_bounds__(NT_F, 2)
             for (int j = 0; j < RUN; ++j) {
 #pragma unroll
                 for (int k = 0; k < 2; ++k) h[k] = f2_fma(a[j][k], h[k], b[j][k]);
-                if (t + j < L) put4<LOAD>(og + (size_t)(t + j) * D, h, c0 + ch, D);
+                if (t + j < L) put4<PIECE>(og + (size_t)(t + j) * D, h, c0 + ch, D);
             }
         };
         // The runs' sums and start values have one buffer each: (A, B) of tile i are written after the
@@ -401,9 +470,10 @@ struct BwdTail {
     uint64_t got[2];
     float2 slot[1];
 };
-// Tiles of the ring: two CTAs share an SM's 227 KB.
-template <typename T>
-constexpr int bwd_stages() { return sizeof(T) == 2 ? 3 : 2; }
+// Tiles of the ring: two CTAs share an SM's 227 KB. Without TMA a thread refills its part of a stage itself,
+// after the walk of the tile before last: three tiles, so that one is always on its way.
+template <typename T, int LOAD>
+constexpr int bwd_stages() { return sizeof(T) == 2 || LOAD != LOAD_TMA ? 3 : 2; }
 
 // The same walk from the sequence's end, by the same three kinds of warps. The states are
 // recomputed inside each tile from the saved ones of every 64 tokens. A tile stays in the ring until
@@ -414,8 +484,9 @@ __global__ void __launch_bounds__(NT_F, 2)
     k_scan_bwd(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mg,
                const __grid_constant__ CUtensorMap md, const ScanArgs P, int cs) {
     extern __shared__ __align__(128) uint8_t smem[];
-    constexpr int kStage = ELEMS * (4 + 2 * (int)sizeof(T)), S = bwd_stages<T>();
-    BwdTail<S>& sm = *reinterpret_cast<BwdTail<S>*>(smem + (LOAD == LOAD_TMA ? S * kStage : 0));
+    constexpr int kStage = ELEMS * (4 + 2 * (int)sizeof(T)), S = bwd_stages<T, LOAD>();
+    constexpr int PIECE = LOAD == LOAD_TMA ? 4 : LOAD;
+    BwdTail<S>& sm = *reinterpret_cast<BwdTail<S>*>(smem + S * kStage);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = cs > 1 ? (int)cluster_rank() : 0;
     const unsigned chain = blockIdx.x / cs;
@@ -449,31 +520,41 @@ __global__ void __launch_bounds__(NT_F, 2)
         T* xo = static_cast<T*>(P.out) + base;
         float* go = P.dg + base;
 
-        // token j of this thread's run in the row's tile
-        auto read = [&](int s, int t, int j, uint64_t (&gv)[2], uint64_t (&xv)[2]) {
-            const float* sg = reinterpret_cast<const float*>(smem + s * kStage) + (tr + j) * CH + ch;
-            if (LOAD == LOAD_TMA) {
-                ld4(sg, gv);
-                ld4(reinterpret_cast<const T*>(smem + s * kStage + ELEMS * 4) + (tr + j) * CH + ch, xv);
-            } else {
-                get4<LOAD>(gg + (size_t)(t + j) * D, gv, t + j < L, c0 + ch, D);
-                get4<LOAD>(xg + (size_t)(t + j) * D, xv, t + j < L, c0 + ch, D);
+        // token j of this thread's run in stage s
+        auto sg = [&](int s, int j) { return reinterpret_cast<float*>(smem + s * kStage) + (tr + j) * CH + ch; };
+        auto sx = [&](int s, int j) {
+            return reinterpret_cast<T*>(smem + s * kStage + ELEMS * 4) + (tr + j) * CH + ch;
+        };
+        auto sd = [&](int s, int j) { return sx(s, j) + ELEMS; };
+        auto fetch = [&](int i) {   // this thread's part of row i's tile, without TMA
+            if (i < P.steps) {
+                const int s = i % S, t = first_token(i) + tr;
+#pragma unroll
+                for (int j = 0; j < RUN; ++j) {
+                    const size_t at = (size_t)(t + j) * D;
+                    const bool row = t + j < L && c0 + ch < D;
+                    fetch4<PIECE>(sg(s, j), row ? gg + at : P.g, row, c0 + ch, D);
+                    fetch4<PIECE>(sx(s, j), row ? xg + at : static_cast<const T*>(P.x), row, c0 + ch, D);
+                    fetch4<PIECE>(sd(s, j), row ? dg + at : static_cast<const T*>(P.dO), row, c0 + ch, D);
+                }
             }
+            fetch_commit();
         };
-        auto read_d = [&](int s, int t, int j, uint64_t (&dv)[2]) {
-            if (LOAD == LOAD_TMA)
-                ld4(reinterpret_cast<const T*>(smem + s * kStage + ELEMS * (4 + sizeof(T))) + (tr + j) * CH + ch, dv);
-            else
-                get4<LOAD>(dg + (size_t)(t + j) * D, dv, t + j < L, c0 + ch, D);
-        };
+        if (LOAD != LOAD_TMA) fetch(0);
         auto compose = [&](int i, uint64_t (&A)[2], uint64_t (&B)[2], uint64_t (&R)[2]) {
-            const int s = i % S, t = first_token(i) + tr;
-            if (LOAD == LOAD_TMA && ok) ok = mbar_wait(&sm.full[s], (i / S) & 1);
+            const int s = i % S;
+            if (LOAD == LOAD_TMA) {
+                if (ok) ok = mbar_wait(&sm.full[s], (i / S) & 1);
+            } else {
+                fetch(i + 1);   // into the stage of row i - 2
+                fetch_wait<1>();
+            }
             uint64_t a[RUN][2];
 #pragma unroll
             for (int j = 0; j < RUN; ++j) {
                 uint64_t gv[2], xv[2], u, inv;
-                read(s, t, j, gv, xv);
+                ld4(sg(s, j), gv);
+                ld4(sx(s, j), xv);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     gate2(gv[k], a[j][k], u);
@@ -485,7 +566,7 @@ __global__ void __launch_bounds__(NT_F, 2)
 #pragma unroll
             for (int j = RUN - 1; j >= 0; --j) {
                 uint64_t dv[2];
-                read_d(s, t, j, dv);
+                ld4(sd(s, j), dv);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) R[k] = f2_mul(a[j][k], j == RUN - 1 ? dv[k] : f2_add(dv[k], R[k]));
             }
@@ -503,7 +584,8 @@ __global__ void __launch_bounds__(NT_F, 2)
 #pragma unroll
             for (int j = 0; j < RUN; ++j) {
                 uint64_t gv[2], xv[2], u, inv;
-                read(s, t, j, gv, xv);
+                ld4(sg(s, j), gv);
+                ld4(sx(s, j), xv);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     gate2(gv[k], a[j][k], u);
@@ -517,7 +599,7 @@ __global__ void __launch_bounds__(NT_F, 2)
 #pragma unroll
             for (int j = RUN - 1; j >= 0; --j) {
                 uint64_t dv[2], ox[2], og[2];
-                read_d(s, t, j, dv);
+                ld4(sd(s, j), dv);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const uint64_t dh = f2_add(dv[k], d[k]);
@@ -526,8 +608,8 @@ __global__ void __launch_bounds__(NT_F, 2)
                     d[k] = f2_mul(a[j][k], dh);
                 }
                 if (t + j < L) {
-                    put4<LOAD>(xo + (size_t)(t + j) * D, ox, c0 + ch, D);
-                    put4<LOAD>(go + (size_t)(t + j) * D, og, c0 + ch, D);
+                    put4<PIECE>(xo + (size_t)(t + j) * D, ox, c0 + ch, D);
+                    put4<PIECE>(go + (size_t)(t + j) * D, og, c0 + ch, D);
                 }
             }
             if (LOAD == LOAD_TMA) {
@@ -606,6 +688,106 @@ __global__ void __launch_bounds__(NT_F, 2)
     if (cs > 1) cluster_sync();
 }
 
+// Short sequences: a tile would be mostly empty, and its warps' hand-overs cost more than the walk itself. One
+// thread walks four channels, kBatch tokens' loads at a time.
+constexpr int NT_W = 64;
+constexpr int kBatch = 8;
+template <typename T, int IN, int PIECE>
+__global__ void __launch_bounds__(NT_W) k_scan_fwd_short(const ScanArgs P) {
+    const int c = (blockIdx.y * NT_W + threadIdx.x) * VEC;
+    const int L = P.L, D = P.D;
+    if (c >= D) return;
+    const size_t bh = blockIdx.x, end = bh * D + c;
+    const T* x = static_cast<const T*>(P.x) + bh * L * D + c;
+    const float* g = P.g + bh * L * D + c;
+    T* o = static_cast<T*>(P.out) + bh * L * D + c;
+    uint64_t h[2] = {0, 0};
+    if (P.first) get4<PIECE>(P.first + end, h, true, c, D);
+    for (int t0 = 0; t0 < L; t0 += kBatch) {
+        if (P.saved && t0 % kSaveEvery == 0)
+            put4<PIECE>(P.saved + (bh * cdiv(L, kSaveEvery) + t0 / kSaveEvery) * D + c, h, c, D);
+        uint64_t gv[kBatch][2], xv[kBatch][2];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            get4<PIECE>(g + (size_t)(t0 + j) * D, gv[j], t0 + j < L, c, D);
+            get4<PIECE>(x + (size_t)(t0 + j) * D, xv[j], t0 + j < L, c, D);
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                uint64_t a, u, inv;
+                gate2(gv[j][k], a, u);
+                h[k] = f2_fma(a, h[k], times_factor2<IN>(in_factor2<IN>(u, inv), xv[j][k]));   // the identity past L
+            }
+            if (P.out && t0 + j < L) put4<PIECE>(o + (size_t)(t0 + j) * D, h, c, D);
+        }
+    }
+    if (P.last) put4<PIECE>(P.last + end, h, c, D);
+}
+// The states h_{t-1} of the forward walk wait in dg, where the same thread's reverse walk replaces them.
+template <typename T, int IN, int PIECE>
+__global__ void __launch_bounds__(NT_W) k_scan_bwd_short(const ScanArgs P) {
+    const int c = (blockIdx.y * NT_W + threadIdx.x) * VEC;
+    const int L = P.L, D = P.D;
+    if (c >= D) return;
+    const size_t bh = blockIdx.x, end = bh * D + c, base = bh * L * D + c;
+    const T *x = static_cast<const T*>(P.x) + base, *dO = static_cast<const T*>(P.dO) + base;
+    const float* g = P.g + base;
+    T* dx = static_cast<T*>(P.out) + base;
+    float* dg = P.dg + base;
+    uint64_t h[2] = {0, 0}, d[2] = {0, 0};
+    if (L > 0) get4<PIECE>(P.saved + bh * cdiv(L, kSaveEvery) * D + c, h, true, c, D);
+    for (int t0 = 0; t0 < L; t0 += kBatch) {
+        uint64_t gv[kBatch][2], xv[kBatch][2];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            get4<PIECE>(g + (size_t)(t0 + j) * D, gv[j], t0 + j < L, c, D);
+            get4<PIECE>(x + (size_t)(t0 + j) * D, xv[j], t0 + j < L, c, D);
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            if (t0 + j < L) put4<PIECE>(dg + (size_t)(t0 + j) * D, h, c, D);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                uint64_t a, u, inv;
+                gate2(gv[j][k], a, u);
+                h[k] = f2_fma(a, h[k], times_factor2<IN>(in_factor2<IN>(u, inv), xv[j][k]));
+            }
+        }
+    }
+    if (P.first) get4<PIECE>(P.first + end, d, true, c, D);
+    for (int t0 = (L - 1) / kBatch * kBatch; L > 0 && t0 >= 0; t0 -= kBatch) {
+        uint64_t gv[kBatch][2], xv[kBatch][2], dv[kBatch][2], hv[kBatch][2];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const size_t at = (size_t)(t0 + j) * D;
+            get4<PIECE>(g + at, gv[j], t0 + j < L, c, D);
+            get4<PIECE>(x + at, xv[j], t0 + j < L, c, D);
+            get4<PIECE>(dO + at, dv[j], t0 + j < L, c, D);
+            get4<PIECE>(dg + at, hv[j], t0 + j < L, c, D);
+        }
+#pragma unroll
+        for (int j = kBatch - 1; j >= 0; --j) {
+            uint64_t ox[2], og[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                uint64_t a, u, inv;
+                gate2(gv[j][k], a, u);
+                const uint64_t m = in_factor2<IN>(u, inv), dh = f2_add(dv[j][k], d[k]);
+                ox[k] = times_factor2<IN>(m, dh);
+                og[k] = f2_mul(slope_fma2<IN>(a, inv, xv[j][k], f2_mul(a, hv[j][k])), dh);
+                d[k] = f2_mul(a, dh);   // unchanged past L: a = 1, dO = 0
+            }
+            if (t0 + j < L) {
+                put4<PIECE>(dx + (size_t)(t0 + j) * D, ox, c, D);
+                put4<PIECE>(dg + (size_t)(t0 + j) * D, og, c, D);
+            }
+        }
+    }
+    if (P.last) put4<PIECE>(P.last + end, d, c, D);
+}
+
 // One token: the state is read and written once. Four channels a thread; the last threads take single
 // ones.
 constexpr int NT_D = 128;
@@ -621,9 +803,9 @@ __global__ void __launch_bounds__(NT_D) k_scan_decode(const T* __restrict__ x, c
         ld4(g + i, gv);
         ld4(state + i, h);
     } else {
-        get4<LOAD_ONE>(x + i, xv, true, 0, (int)(n - i));
-        get4<LOAD_ONE>(g + i, gv, true, 0, (int)(n - i));
-        get4<LOAD_ONE>(state + i, h, true, 0, (int)(n - i));
+        get4<1>(x + i, xv, true, 0, (int)(n - i));
+        get4<1>(g + i, gv, true, 0, (int)(n - i));
+        get4<1>(state + i, h, true, 0, (int)(n - i));
     }
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -635,8 +817,8 @@ __global__ void __launch_bounds__(NT_D) k_scan_decode(const T* __restrict__ x, c
         st4(state + i, h);
         st4(o + i, h);
     } else {
-        put4<LOAD_ONE>(state + i, h, 0, (int)(n - i));
-        put4<LOAD_ONE>(o + i, h, 0, (int)(n - i));
+        put4<1>(state + i, h, 0, (int)(n - i));
+        put4<1>(o + i, h, 0, (int)(n - i));
     }
 }
 
@@ -710,8 +892,8 @@ cudaError_t launch_walk(const gla_problem* p, ScanArgs P, const CUtensorMap (&ma
     const long long chains = (long long)p->B * p->H * P.nblk;
     const int tiles = cdiv(P.L, TT);
     constexpr int kStage = ELEMS * (4 + (BWD ? 2 : 1) * (int)sizeof(T));
-    constexpr size_t ring = LOAD == LOAD_TMA ? (size_t)kStage * (BWD ? bwd_stages<T>() : kFwdStages) : 0;
-    constexpr size_t tail = BWD ? sizeof(BwdTail<bwd_stages<T>()>) : sizeof(FwdTail);
+    constexpr size_t ring = (size_t)kStage * (BWD ? bwd_stages<T, LOAD>() : kFwdStages);
+    constexpr size_t tail = BWD ? sizeof(BwdTail<bwd_stages<T, LOAD>()>) : sizeof(FwdTail);
     auto smem = [&](int c) { return ring + tail + (c > 1 ? 2 * CH * sizeof(float2) * c : 0); };
     auto kern = [] {
         if constexpr (BWD) return k_scan_bwd<T, IN, LOAD>;
@@ -723,6 +905,9 @@ cudaError_t launch_walk(const gla_problem* p, ScanArgs P, const CUtensorMap (&ma
     if (e != cudaSuccess) return e;
     int dev = 0;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    if (known[dev][1].load(std::memory_order_relaxed) == 0 &&
+        (e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
+        return e;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(NT_F);
     cfg.stream = st;
@@ -733,7 +918,7 @@ cudaError_t launch_walk(const gla_problem* p, ScanArgs P, const CUtensorMap (&ma
     cfg.numAttrs = 1;
     int cs = 1;
     long long best = -1;
-    for (int c = 1; c <= kMaxCluster && (c == 1 || c <= tiles); ++c) {
+    for (int c = 1; c <= kMaxCluster && (c == 1 || c <= tiles); c = c == 8 ? 16 : c + 1) {
         const int slots = resident_ctas(kern, cfg, c, smem(c), known[dev]);
         if (slots <= 0) continue;
         const long long cost = (chains * c + slots - 1) / slots * (cdiv(tiles, c) + kFill);
@@ -750,16 +935,40 @@ cudaError_t launch_walk(const gla_problem* p, ScanArgs P, const CUtensorMap (&ma
     return e;
 }
 
+template <typename T, int IN, int PIECE, bool BWD>
+cudaError_t launch_short(const gla_problem* p, const ScanArgs& P, cudaStream_t st) {
+    const dim3 grid((unsigned)(p->B * p->H), cdiv(P.D, NT_W * VEC));
+    if constexpr (BWD)
+        GLA_LAUNCH("scan_bwd_short", st, (k_scan_bwd_short<T, IN, PIECE><<<grid, NT_W, 0, st>>>(P)));
+    else
+        GLA_LAUNCH("scan_fwd_short", st, (k_scan_fwd_short<T, IN, PIECE><<<grid, NT_W, 0, st>>>(P)));
+    return cudaGetLastError();
+}
+
+// Whether threads walk sequences alone: up to 64 tokens, when their batches of loads (about 1.6 us each, forward) cost
+// less than the waves of CTAs of mostly empty tiles (about 3 us each, two CTAs an SM). Measured, us forward /
+// training pair, alone and by tiles: 1 x 4 heads x 64, 8 tokens 1.9 / 6.1 and 2.7 / 6.8, 32 tokens 4.8 / 15 and
+// 3.0 / 6.7; 64 x 4096 channels, 32 tokens 20 / 68 and 77 / 182, 128 tokens 79 / 330 and 88 / 225.
+bool is_short(const gla_problem* p) {
+    const long long chains = (long long)p->B * p->H * cdiv(p->Dk, CH), at_once = 2 * tc::num_sms();
+    return p->L <= 64 && cdiv(p->L, kBatch) < 2 * ((chains + at_once - 1) / at_once);
+}
+
 template <typename T, int IN, bool BWD>
 cudaError_t walk(const gla_problem* p, const ScanArgs& P, cudaStream_t st) {
     CUtensorMap maps[3] = {};
     const int BH = p->B * p->H, D = P.D, L = P.L;
+    if (is_short(p))
+        return D % 4 == 0   ? launch_short<T, IN, 4, BWD>(p, P, st)
+               : D % 2 == 0 ? launch_short<T, IN, 2, BWD>(p, P, st)
+                            : launch_short<T, IN, 1, BWD>(p, P, st);
     // TMA boxes need rows of whole 16-byte pieces, and are not used for rows shorter than a box
-    if (D % (16 / (int)sizeof(T)) == 0 && D >= CH && L > 0 && scan_map<T>(&maps[0], P.x, D, L, BH) &&
+    if (D % (16 / (int)sizeof(T)) == 0 && D >= CH && scan_map<T>(&maps[0], P.x, D, L, BH) &&
         scan_map<float>(&maps[1], P.g, D, L, BH) && (!BWD || scan_map<T>(&maps[2], P.dO, D, L, BH)))
         return launch_walk<T, IN, LOAD_TMA, BWD>(p, P, maps, st);
-    return D % 4 == 0 ? launch_walk<T, IN, LOAD_VEC4, BWD>(p, P, maps, st)
-                      : launch_walk<T, IN, LOAD_ONE, BWD>(p, P, maps, st);
+    return D % 4 == 0   ? launch_walk<T, IN, LOAD_4, BWD>(p, P, maps, st)
+           : D % 2 == 0 ? launch_walk<T, IN, LOAD_2, BWD>(p, P, maps, st)
+                        : launch_walk<T, IN, LOAD_1, BWD>(p, P, maps, st);
 }
 
 cudaError_t fwd(const gla_problem* p, int input, const void* x, const float* g, const float* h0, void* o, float* hT,

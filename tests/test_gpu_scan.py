@@ -130,7 +130,8 @@ def check(B, H, L, D, io, kind, gates, seed, h0=True, save=True):
 
 SIZES = [(1, 1, 1, 1), (2, 3, 1, 64), (1, 1, 2, 8), (2, 3, 63, 5), (1, 2, 64, 64), (1, 2, 65, 100), (2, 1, 127, 36),
          (1, 1, 128, 33), (2, 2, 129, 40), (1, 1, 300, 130), (1, 3, 517, 72), (2, 2, 1021, 24), (1, 2, 2049, 64),
-         (1, 1, 4500, 96), (1, 1, 333, 257), (5, 7, 200, 16)]
+         (1, 1, 4500, 96), (1, 1, 333, 257), (5, 7, 200, 16), (1, 1, 700, 74), (2, 1, 900, 130), (3, 2, 8, 64), (3, 2, 8, 66),
+         (3, 2, 7, 67), (2, 2, 9, 40), (20, 1, 24, 1280), (20, 1, 25, 1282), (20, 1, 23, 1281), (60, 1, 64, 516)]
 
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])
