@@ -918,7 +918,7 @@ cudaError_t launch_walk(const gla_problem* p, ScanArgs P, const CUtensorMap (&ma
     cfg.numAttrs = 1;
     int cs = 1;
     long long best = -1;
-    for (int c = 1; c <= kMaxCluster && (c == 1 || c <= tiles); c = c == 8 ? 16 : c + 1) {
+    for (int c = 1; c <= kMaxCluster && (c == 1 || c <= tiles); ++c) {
         const int slots = resident_ctas(kern, cfg, c, smem(c), known[dev]);
         if (slots <= 0) continue;
         const long long cost = (chains * c + slots - 1) / slots * (cdiv(tiles, c) + kFill);
