@@ -739,6 +739,126 @@ def run_mlstm(args, world, rank, local):
     print(json.dumps(base), flush=True)
 
 
+def layer_oracle_sample(seed, heads):
+    """Times the float64 oracles of the layer step's operators on `heads` heads of one sequence (the norm
+    before the block over those heads' channels). Returns (tokens_equivalent, seconds)."""
+    from oracle import norms, scan
+    c = I.LAYER
+    x = {k: v.double().numpy() for k, v in I.make_layer_inputs(1, heads, c["L"], c["D"], c["dtype"], seed).items()}
+    t0 = time.perf_counter()
+    r, _ = norms.addnorm_fwd(x["x"], x["res"], x["rs"], x["w1"], 1.0, "rms", 1e-6)
+    o, _ = scan.scan_fwd(x["xs"], x["g"], None, "complement")
+    norms.headnorm_fwd(o, x["z"], x["w2"], "silu", "rms", 1e-6)
+    d = norms.headnorm_bwd(o, x["z"], x["w2"], x["dy"], "silu", "rms", 1e-6)
+    scan.scan_bwd(x["xs"], x["g"], None, d["do"], None, "complement")
+    norms.addnorm_bwd(x["x"].reshape(c["L"], -1), r.reshape(c["L"], -1), x["rs"], x["w1"],
+                      x["dn"].reshape(c["L"], -1), x["dr"].reshape(c["L"], -1), 1.0, "rms", 1e-6)
+    return c["L"] * heads / c["H"], time.perf_counter() - t0
+
+
+def run_layer(args, world, rank, local):
+    """What a layer with a vector-state cell runs besides its projections, forward and backward: residual
+    sum and norm (gla_addnorm), gated linear recurrence (gla_scan, training pair), norm and gate
+    (gla_headnorm), B=4 H=16 L=4096 D=256 bf16 on HBM-resident inputs."""
+    c = I.LAYER
+    B, H, L, D, e = c["B"], c["H"], c["L"], c["D"], 2
+    n = B * H * L * D
+    # every call's inputs read and outputs written: addnorm x, res -> r, y; scan x, g -> o; headnorm o, z -> y;
+    # headnorm bwd o, z, dy -> do, dz; scan bwd x, g, do -> dx, dg; addnorm bwd x, r, dy, dr -> dres, dx
+    by = n * (4 * e + (2 * e + 4) + 3 * e + 5 * e + (3 * e + 8) + 6 * e)
+    base = {"metric": "layer step fwd+bwd tokens/s", "unit": "tokens/s", "n_gpus": world, "steps": args.steps,
+            "warmup": args.warmup, "higher_is_better": True, "scaling": "weak", "vs_baseline": None,
+            "dtype": c["dtype"], "data": "synthetic (seeded; linear_rnn_b200/inputs.py)",
+            "config": {"workload": f"layer: addnorm, scan, headnorm forward+backward, B={B} H={H} L={L} D={D} bf16",
+                       "global_batch": B * world, "seq_len": L, "parallelism": f"replicas x{world}",
+                       "l2": "256 MiB L2 flush between steps, outside the per-step events; inputs > L2"}}
+    if args.impl == "reference":
+        if rank != 0:
+            return
+        for _ in range(args.warmup):
+            layer_oracle_sample(0, 1)
+        tok = tot = 0.0
+        for i in range(args.steps):
+            t, dt = layer_oracle_sample(i, 1)
+            tok += t
+            tot += dt
+        val = tok / tot
+        base.update({"impl": "reference", "value": val, "ms_per_step": 1e3 * B * L / val, "dtype": "f64",
+                     "gpu_launches": 0,
+                     "cpu_baseline": {"value": val, "unit": "tokens/s", "cores": blas_threads(), "kind": "oracle",
+                                      "sample": f"1 of {B * H} heads, full L={L}, fwd+bwd per step"},
+                     "e2e": {"value": val, "unit": "tokens/s", "h2d_bytes_per_step": 0, "d2h_bytes_per_step": 0}})
+        print(json.dumps(base), flush=True)
+        return
+    from linear_rnn_b200 import ops
+    torch.cuda.set_device(local)
+    dev = torch.device("cuda", local)
+    x = I.make_layer_inputs(B, H, L, D, c["dtype"], seed=rank)
+    xd = {k: v.to(dev) for k, v in x.items()}
+    saved = torch.empty(ops.gla_scan_saved_bytes(ops.make_scan_problem(xd["xs"])), dtype=torch.uint8, device=dev)
+
+    def step(a=xd):
+        r, y = ops.gla_addnorm_fwd(a["x"], a["res"], a["w1"], rscale=a["rs"])
+        o, _ = ops.gla_scan_fwd(a["xs"], a["g"], input="complement", saved_states=saved, output_final_state=False)
+        u = ops.gla_headnorm_fwd(o, a["z"], a["w2"])
+        g3 = ops.gla_headnorm_bwd(o, a["z"], a["w2"], a["dy"])
+        g2 = ops.gla_scan_bwd(a["xs"], a["g"], None, g3["do"], input="complement", saved_states=saved,
+                              output_dh0=False)
+        g1 = ops.gla_addnorm_bwd(a["x"], r, a["w1"], a["dn"], a["dr"], rscale=a["rs"])
+        return [y, u, g3["dz"], g3["dw"], g2["dx"], g2["dg"], *g1.values()]
+
+    flush = torch.empty(256 << 20, dtype=torch.uint8, device=dev)
+    sampler = ClockSampler(local)
+    sampler.start()
+    time.sleep(0.3)
+    for i in range(args.warmup):
+        flush.fill_(i & 0xFF)
+        step()
+    torch.cuda.synchronize()
+    tot, per, launches, _ = time_steps(step, flush, args.steps, world)
+    _, _, _, kp = time_steps(step, flush, args.steps, world, per_kernel=True)
+    clocks = sampler.stop()
+    tot = max_over_ranks(tot, dev)
+    e2e = None
+    if not args.no_e2e:
+        xh = {k: v.pin_memory() for k, v in x.items()}
+        h2d = sum(t.numel() * t.element_size() for t in xh.values())
+        d2h = 0
+
+        def e2e_step():
+            nonlocal d2h
+            d2h = sum(t.numel() * t.element_size()
+                      for t in ops._to_host(step({k: t.to(dev, non_blocking=True) for k, t in xh.items()})))
+
+        for _ in range(2):
+            e2e_step()
+        torch.cuda.synchronize()
+        s0, s1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        s0.record()
+        for _ in range(args.steps):
+            e2e_step()
+        s1.record()
+        torch.cuda.synchronize()
+        e_ms = max_over_ranks(s0.elapsed_time(s1), dev)
+        e2e = {"value": B * L * args.steps * world / (e_ms / 1e3), "unit": "tokens/s",
+               "h2d_bytes_per_step": int(h2d), "d2h_bytes_per_step": int(d2h)}
+    if rank != 0:
+        return
+    peaks, peak_src = load_peaks()
+    t = tot / args.steps / 1e3
+    base.update({"value": B * L * world / t, "ms_per_step": tot / args.steps, "e2e": e2e,
+                 "gpu_launches": int(launches), "clocks": clocks,
+                 "step_roofline": {"gbs_compulsory": by / t / 1e9, "roofline_us": by / (peaks["hbm_gbs"] * 1e9) * 1e6,
+                                   "frac": by / (peaks["hbm_gbs"] * 1e9) / t, "peak_source": peak_src,
+                                   "bound": "hbm (every call's inputs and outputs once)"},
+                 "kernels": {k: {"launches": m, "avg_us": 1e3 * ms / m} for k, (m, ms) in sorted(kp.items())}})
+    if world == 1 and not args.no_cpu_baseline:
+        tk, dt = layer_oracle_sample(0, 1)
+        base["cpu_baseline"] = {"value": tk / dt, "unit": "tokens/s", "cores": blas_threads(), "kind": "oracle",
+                                "sample": f"1 of {B * H} heads, full L={L}, fwd+bwd, float64, {dt:.1f} s"}
+    print(json.dumps(base), flush=True)
+
+
 def time_steps(step, flush, steps, world, per_kernel=False, flush_l2=True):
     """K steps bracketed by barrier + synchronize; per-step CUDA events on the stream, with the
     256 MiB L2 flush before each step outside the events (flush_l2=False: warm L2). per_kernel:
@@ -812,7 +932,7 @@ def main():
     ap.add_argument("--steps", type=int, default=10)
     ap.add_argument("--warmup", type=int, default=3)
     ap.add_argument("--workload", default="c3",
-                    choices=sorted(I.WORKLOADS) + ["decode", "deltanet", "shard", "mlstm"])
+                    choices=sorted(I.WORKLOADS) + ["decode", "deltanet", "shard", "mlstm", "layer"])
     ap.add_argument("--impl", default="ours", choices=["ours", "reference"])
     ap.add_argument("--plan", default="auto", choices=["auto", "simt", "tc"])
     ap.add_argument("--no-e2e", action="store_true")
@@ -824,12 +944,14 @@ def main():
     args = ap.parse_args()
     if args.warmup < 3:
         args.warmup = 3
-    if args.workload in ("deltanet", "shard", "mlstm"):
+    if args.workload in ("deltanet", "shard", "mlstm", "layer"):
         world, rank, local = dist_setup()
         if args.workload == "deltanet":
             run_deltanet(args, world, rank, local)
         elif args.workload == "mlstm":
             run_mlstm(args, world, rank, local)
+        elif args.workload == "layer":
+            run_layer(args, world, rank, local)
         elif args.impl != "reference":
             run_shard(args, world, rank, local)
         elif rank == 0:

@@ -192,3 +192,24 @@ def make_mlstm_inputs(w: Workload, seed: int = 0, itil_shift: float = 0.0) -> Di
     itil = randn(B, H, L) + itil_shift
     dh = _round_io(randn(B, H, L, Dv), w.dtype) if w.backward else None
     return {"q": q, "k": k, "v": v, "g": g, "itil": itil, "dh": dh}
+
+
+# What a layer with a vector-state cell runs besides its projections: the residual sum and norm before
+# the block, the gated linear recurrence, the norm and gate after it, at the main workload's sizes.
+LAYER = dict(B=4, H=16, L=4096, D=256, dtype="bf16")
+
+
+def make_layer_inputs(B: int, H: int, L: int, D: int, dtype: str, seed: int = 0) -> Dict[str, torch.Tensor]:
+    """Seeded inputs of that layer step, drawn in this order: x, res [B,L,H*D], xs [B,H,L,D], gate
+    pre-activation, z [B,L,H,D], dy (of the gated output) [B,L,H,D], dn, dr (of the norm's output and of
+    the residual) [B,L,H*D]: standard normals; w1, rs [H*D] and w2 [D] fp32 around 1 and 0.5. The gates are
+    logsigmoid(N(0,1))/16 in fp32."""
+    gen = torch.Generator().manual_seed(seed)
+    n = lambda *shape: torch.randn(*shape, generator=gen)
+    M = H * D
+    out = {"x": _round_io(n(B, L, M), dtype), "res": _round_io(n(B, L, M), dtype),
+           "xs": _round_io(n(B, H, L, D), dtype), "g": torch.nn.functional.logsigmoid(n(B, H, L, D)) / 16.0,
+           "z": _round_io(n(B, L, H, D), dtype), "dy": _round_io(n(B, L, H, D), dtype),
+           "dn": _round_io(n(B, L, M), dtype), "dr": _round_io(n(B, L, M), dtype)}
+    out.update(w1=1.0 + 0.2 * n(M), rs=0.5 + 0.1 * n(M), w2=1.0 + 0.2 * n(D))
+    return out
