@@ -308,7 +308,7 @@ def _take(name, t, shape, dtype, device):
     """A checked argument on `device`: `shape` and `dtype` exactly, contiguous, or None."""
     if t is None:
         return None
-    if t.dtype != dtype or t.shape != shape:
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
     if t.device != device:
         if t.is_cuda:

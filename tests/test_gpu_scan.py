@@ -5,10 +5,11 @@ One token's step rounds a (relative error da), m (dm), the product m x, and the 
 tree of products instead of a token-by-token walk only regroups those roundings. So the error
 of h_t is at most e_t = a_t e_{t-1} + (da + 2u) a_t H_{t-1} + (dm + 2u) |m_t x_t|, with H the same
 recurrence over absolute values and u = 2^-24; another 40 u H_t covers the levels of the tree. The
-gate: CUDA's bound on __expf is 2 + 1.173 |g| ulp (an ulp at most 2^-23), and for |g| < 0.35
-the series and the subtraction stay below 2 ulp, so da = (2 + 1.2 |g|) 2^-23. 1 - a: where
-|g| >= 0.35, a's error over 1 - a >= 0.295 is below 6 ulp, and less for larger |g|; its root
-halves that and adds two roundings: dm = 6 * 2^-23 for both. The slope a^2 / m: 2 da + dm + 3u.
+gate: for -0.30 <= g <= 0.05 a = 1 - t with t within 2u of itself, elsewhere the hardware's 2^x (2^-22)
+of a product that one rounding moves by |g| u: da = (2 + 1.2 |g|) 2^-23 covers both. 1 - a at
+g < -0.30, where it is at least 0.259: a's error 0.741 * 2.15 * 2^-23 and the subtraction's 2^-26 over
+that are 6.7 * 2^-23, and less for larger |g|; its root halves that and adds 2^-22: dm = 7 * 2^-23 for
+both. The slope a^2 / m: 2 da + dm + 3u.
 The backward's dh obeys the same recurrence in reverse. A stored value adds half a step of its
 type: finfo(t).eps / 2.
 """
@@ -55,7 +56,7 @@ def bounds(x, g, h0, dO, dhT, kind, io):
     a = np.exp(g)
     m, dm = scan.input_factor(g, kind)
     da = (2 + 1.2 * np.where(np.isfinite(g), np.abs(g), 0)) * ULP
-    rm = 0.0 if kind == "plain" else 6 * ULP
+    rm = 0.0 if kind == "plain" else 7 * ULP
     zero = np.zeros(x.shape[:2] + x.shape[3:])
     o, _ = scan.scan_fwd(x, g, h0, kind)
     H, e = errors_of_recurrence(a, da, np.abs(m * x), rm, zero if h0 is None else np.abs(h0))
