@@ -10,8 +10,10 @@ namespace {
 
 using namespace norm;
 
+// Blocks of 256 threads per SM that the registers leave room for, 16384 x 4096: 4 with an fp32 residual (2: 139 us,
+// 3: 143, 4: 135), 2 with everything in bf16 (2: 100 us, 3: 104, 4: 105).
 template <typename T, typename R, int VEC, int NV, int S, int KIND, int MAXT>
-__global__ void __launch_bounds__(MAXT, 1024 / MAXT)   // 64 registers: 4 blocks of 256 threads (134 us, 148 with 3)
+__global__ void __launch_bounds__(MAXT, MAXT == 256 && VEC == 8 ? 2 : 1024 / MAXT)
     k_addnorm_fwd(const T* __restrict__ x, const R* res, const float* __restrict__ rscale,
                   const float* __restrict__ w, R* r_out, T* __restrict__ y, int rows, int D, int G, float alpha,
                   float eps) {
@@ -104,7 +106,7 @@ __global__ void __launch_bounds__(MAXT, 1024 / MAXT)   // 64 registers: 4 blocks
 }
 
 template <typename T, typename R, int VEC, int NV, int S, int KIND, int MAXT>
-__global__ void __launch_bounds__(MAXT)
+__global__ void __launch_bounds__(MAXT < 512 ? 512 : MAXT)   // 16384 x 2048: 79 us; bounded by 256 threads, 2 blocks 88
     k_addnorm_bwd(const T* __restrict__ x, const R* __restrict__ r_in, const float* __restrict__ rscale,
                   const float* __restrict__ w, const T* __restrict__ dy, const R* dr, R* dres, T* __restrict__ dx,
                   float* __restrict__ pdw, float* __restrict__ pds, int rows, int D, int G, float alpha, float eps) {

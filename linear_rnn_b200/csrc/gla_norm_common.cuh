@@ -441,25 +441,31 @@ template <int V, int N, int S, int M> struct Shape {
     static constexpr int vec = V, nv = N, stages = S, maxt = M;
 };
 // BF16, F32: every operand of the row has that type, so pieces of 8, and a ring of single elements, exist too.
-// Without a ring up to 1024 threads: with 16 elements each they spill; only rows beyond 8192 elements.
+// Blocks of up to 256 threads (D <= 4096 with pieces of 4 or 8) have kernels of their own, which need not fit their
+// registers into a larger block's share. Without a ring up to 1024 threads: with 16 elements each they
+// spill; only rows beyond 8192 elements, or too long for two stages.
+template <int V, int N, int S, typename F>
+cudaError_t by_block(const RowPlan& p, F&& f) {
+    return p.threads <= 256 ? f(Shape<V, N, S, 256>{}) : f(Shape<V, N, S, 512>{});
+}
 template <bool BF16, bool F32, typename F>
 cudaError_t by_shape(const RowPlan& p, int stages, F&& f) {
     if (p.vec == 1) {
         if (p.nv == 16) return f(Shape<1, 16, 0, 1024>{});
         if constexpr (F32)
-            if (stages == 3) return f(Shape<1, 4, 3, 512>{});
-        return f(Shape<1, 4, 0, 512>{});
+            if (stages == 3) return by_block<1, 4, 3>(p, f);
+        return by_block<1, 4, 0>(p, f);
     }
     if (p.vec == 2) {
         if (p.nv == 8) return f(Shape<2, 8, 0, 1024>{});
-        return stages == 3 ? f(Shape<2, 4, 3, 512>{}) : f(Shape<2, 4, 0, 512>{});
+        return stages == 3 ? by_block<2, 4, 3>(p, f) : f(Shape<2, 4, 0, 512>{});
     }
     if constexpr (BF16)
         if (p.vec == 8)
-            return stages == 3   ? f(Shape<8, 2, 3, 512>{})
+            return stages == 3   ? by_block<8, 2, 3>(p, f)
                    : stages == 2 ? f(Shape<8, 2, 2, 512>{})
                                  : f(Shape<8, 2, 0, 1024>{});
-    return stages == 3   ? f(Shape<4, 4, 3, 512>{})
+    return stages == 3   ? by_block<4, 4, 3>(p, f)
            : stages == 2 ? f(Shape<4, 4, 2, 512>{})
                          : f(Shape<4, 4, 0, 1024>{});
 }
