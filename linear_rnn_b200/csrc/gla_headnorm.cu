@@ -276,6 +276,8 @@ cudaError_t by_act(int act, F&& f) {
                                : f(std::integral_constant<int, GLA_ACT_SIGMOID>{});
 }
 
+RowPlan plan(const gla_norm_problem* p) { return row_plan(p->D, p->io == GLA_BF16, p->io == GLA_F32); }
+
 gla_status check(const gla_norm_problem* p) {
     const gla_status s = check_common(p);
     if (s != GLA_OK) return s;
@@ -293,7 +295,7 @@ extern "C" {
 
 size_t gla_headnorm_workspace_bytes(const gla_norm_problem* p) {
     if (check(p) != GLA_OK) return 0;
-    const int P = p->H ? row_blocks(row_plan(p->D, p->io == GLA_BF16, p->io == GLA_F32), (long long)p->B * p->L, p->H) : 0;
+    const int P = p->H ? row_blocks(plan(p), (long long)p->B * p->L, p->H) : 0;
     return 256 + (size_t)P * p->H * p->D * 4;
 }
 
@@ -307,7 +309,7 @@ gla_status gla_headnorm_fwd(const gla_norm_problem* p, const void* o, const void
     if (tokens == 0 || p->H == 0) return GLA_OK;
     if (!o || !y) return GLA_ERR_INVALID_ARG;
     cudaStream_t st = (cudaStream_t)stream;
-    const RowPlan rp = row_plan(p->D, p->io == GLA_BF16, p->io == GLA_F32);
+    const RowPlan rp = plan(p);
     const cudaError_t e = by_io(p->io, [&](auto tv) {
         using T = decltype(tv);
         const int thread_bytes = 2 * rp.nv * rp.vec * (int)sizeof(T);
@@ -345,7 +347,7 @@ gla_status gla_headnorm_bwd(const gla_norm_problem* p, const void* o, const void
     cudaStream_t st = (cudaStream_t)stream;
     const int tokens = p->B * p->L;
     if (p->H == 0 && (!dw || p->w_per_head)) return GLA_OK;
-    const RowPlan rp = row_plan(p->D, p->io == GLA_BF16, p->io == GLA_F32);
+    const RowPlan rp = plan(p);
     int P = p->H ? row_blocks(rp, tokens, p->H) : 0;
     float* pdw = dw ? static_cast<float*>(ws) : nullptr;
     cudaError_t e = cudaSuccess;

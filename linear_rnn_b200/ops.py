@@ -496,7 +496,8 @@ def gla_addnorm_fwd(x, res=None, w=None, *, rscale=None, alpha: float = 1.0, kin
 
 
 def gla_addnorm_bwd(x, r, w, dy, dr=None, *, rscale=None, alpha: float = 1.0, kind: str = "rms", eps: float = 1e-6,
-                    output_dx: bool = True, workspace: Optional[torch.Tensor] = None) -> Dict[str, Optional[torch.Tensor]]:
+                    output_dx: bool = True,
+                    workspace: Optional[torch.Tensor] = None) -> Dict[str, Optional[torch.Tensor]]:
     """Gradients of sum(dy * y) + sum(dr * r) of gla_addnorm_fwd at the r it returned: dict dres
     (r's dtype), dx (dy's dtype; None when output_dx is False: with alpha = 1, no rscale and one
     dtype it equals dres), dw (fp32 [D], None without w) and drscale (fp32 [D], None without
