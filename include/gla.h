@@ -410,7 +410,8 @@ typedef struct {
  *   NULL). drscale needs rscale. The row sums of dw and drscale are taken in a fixed order, without
  *   atomics. Zero rows give dw = drscale = 0.
  * ws: gla_addnorm_workspace_bytes(p) bytes of caller-owned device memory (0 when p is invalid or
- *   unsupported), the backward's partial sums. Otherwise outputs may not overlap inputs or ws.
+ *   unsupported), the backward's partial sums; with 256 bytes or less none is needed (NULL, 0).
+ *   Otherwise outputs may not overlap inputs or ws.
  * All pointers 16-byte aligned device memory. Asynchronous on `stream`.
  * Errors: GLA_ERR_INVALID_ARG (null or misaligned pointer, bad enum, size, eps), GLA_ERR_UNSUPPORTED
  *   (D, dtypes), GLA_ERR_WORKSPACE, GLA_ERR_CUDA. */

@@ -294,7 +294,7 @@ extern "C" {
 size_t gla_addnorm_workspace_bytes(const gla_norm_problem* p) {
     if (check(p) != GLA_OK) return 0;
     const int P = row_blocks(plan(p), (long long)p->B * p->L, 1);
-    return 256 + 2 * align_up((size_t)P * p->D * 4, 256);
+    return P > 1 ? 256 + 2 * align_up((size_t)P * p->D * 4, 256) : 256;
 }
 
 gla_status gla_addnorm_fwd(const gla_norm_problem* p, const void* x, const void* res, const float* rscale,
@@ -340,16 +340,18 @@ gla_status gla_addnorm_bwd(const gla_norm_problem* p, const void* x, const void*
     const gla_status s = check(p);
     if (s != GLA_OK) return s;
     const void* const ptrs[] = {x, r, rscale, w, dy, dr, dres, dx, dw, drscale, ws};
-    if (!all_aligned(ptrs) || !ws) return GLA_ERR_INVALID_ARG;
-    if (drscale && !rscale) return GLA_ERR_INVALID_ARG;
-    if (ws_bytes < gla_addnorm_workspace_bytes(p)) return GLA_ERR_WORKSPACE;
-    cudaStream_t st = (cudaStream_t)stream;
     const int rows = p->B * p->L;
     const RowPlan rp = plan(p);
     int P = row_blocks(rp, rows, 1);
-    float* pdw = dw ? static_cast<float*>(ws) : nullptr;
-    float* pds = drscale ? reinterpret_cast<float*>(static_cast<char*>(ws) + align_up((size_t)P * p->D * 4, 256))
-                         : nullptr;
+    const bool direct = P == 1;   // a single block's sums are the result
+    if (!all_aligned(ptrs) || (!ws && P > 1)) return GLA_ERR_INVALID_ARG;
+    if (drscale && !rscale) return GLA_ERR_INVALID_ARG;
+    if (P > 1 && ws_bytes < gla_addnorm_workspace_bytes(p)) return GLA_ERR_WORKSPACE;
+    cudaStream_t st = (cudaStream_t)stream;
+    float* pdw = !dw || direct ? dw : static_cast<float*>(ws);
+    float* pds = !drscale || direct
+                     ? drscale
+                     : reinterpret_cast<float*>(static_cast<char*>(ws) + align_up((size_t)P * p->D * 4, 256));
     cudaError_t e = cudaSuccess;
     if (rows > 0) {
         if (!r || !dy || (drscale && !x)) return GLA_ERR_INVALID_ARG;
@@ -378,7 +380,7 @@ gla_status gla_addnorm_bwd(const gla_norm_problem* p, const void* x, const void*
             });
         });
     }
-    if (e == cudaSuccess) e = colsum(pdw, dw, pds, drscale, P, p->D, p->D, st);
+    if (e == cudaSuccess && !direct) e = colsum(pdw, dw, pds, drscale, P, p->D, p->D, st);
     return record_cuda(e, "addnorm backward");
 }
 

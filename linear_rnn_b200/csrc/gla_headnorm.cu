@@ -278,6 +278,9 @@ cudaError_t by_act(int act, F&& f) {
 
 RowPlan plan(const gla_norm_problem* p) { return row_plan(p->D, p->io == GLA_BF16, p->io == GLA_F32); }
 
+// Whether the blocks' column sums are the result already: one block, or one per head and head's weights.
+bool is_direct(const gla_norm_problem* p, int P) { return P == 1 && (p->w_per_head || p->H == 1); }
+
 gla_status check(const gla_norm_problem* p) {
     const gla_status s = check_common(p);
     if (s != GLA_OK) return s;
@@ -296,7 +299,7 @@ extern "C" {
 size_t gla_headnorm_workspace_bytes(const gla_norm_problem* p) {
     if (check(p) != GLA_OK) return 0;
     const int P = p->H ? row_blocks(plan(p), (long long)p->B * p->L, p->H) : 0;
-    return 256 + (size_t)P * p->H * p->D * 4;
+    return is_direct(p, P) ? 256 : 256 + (size_t)P * p->H * p->D * 4;
 }
 
 gla_status gla_headnorm_fwd(const gla_norm_problem* p, const void* o, const void* z, const float* w, void* y,
@@ -342,14 +345,15 @@ gla_status gla_headnorm_bwd(const gla_norm_problem* p, const void* o, const void
     const gla_status s = check(p);
     if (s != GLA_OK) return s;
     const void* const ptrs[] = {o, z, w, dy, d_o, dz, dw, ws};
-    if (!all_aligned(ptrs) || !ws || (dz && !z)) return GLA_ERR_INVALID_ARG;
-    if (ws_bytes < gla_headnorm_workspace_bytes(p)) return GLA_ERR_WORKSPACE;
-    cudaStream_t st = (cudaStream_t)stream;
     const int tokens = p->B * p->L;
-    if (p->H == 0 && (!dw || p->w_per_head)) return GLA_OK;
     const RowPlan rp = plan(p);
     int P = p->H ? row_blocks(rp, tokens, p->H) : 0;
-    float* pdw = dw ? static_cast<float*>(ws) : nullptr;
+    const bool direct = is_direct(p, P), partials = P > 0 && !direct;
+    if (!all_aligned(ptrs) || (!ws && partials) || (dz && !z)) return GLA_ERR_INVALID_ARG;
+    if (partials && ws_bytes < gla_headnorm_workspace_bytes(p)) return GLA_ERR_WORKSPACE;
+    cudaStream_t st = (cudaStream_t)stream;
+    if (p->H == 0 && (!dw || p->w_per_head)) return GLA_OK;
+    float* pdw = !dw || direct ? dw : static_cast<float*>(ws);
     cudaError_t e = cudaSuccess;
     if (tokens > 0 && p->H > 0) {
         if (!o || !dy || !d_o) return GLA_ERR_INVALID_ARG;
@@ -379,7 +383,7 @@ gla_status gla_headnorm_bwd(const gla_norm_problem* p, const void* o, const void
             });
         });
     }
-    if (e == cudaSuccess && dw)
+    if (e == cudaSuccess && dw && !direct)
         e = p->w_per_head ? colsum(pdw, dw, nullptr, nullptr, P, (size_t)p->H * p->D, p->H * p->D, st)
                           : colsum(pdw, dw, nullptr, nullptr, P * p->H, p->D, p->D, st);
     return record_cuda(e, "headnorm backward");

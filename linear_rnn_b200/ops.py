@@ -300,29 +300,36 @@ def gla_deltanet_bwd(q, k, v, beta, h0, dO, dhT=None, *, scale: Optional[float] 
     return out
 
 
-def _addr(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
+# The operators below are also called where a pass takes a few microseconds on the GPU, so their
+# host work is kept short: descriptors are looked up by sizes and types, and every tensor is
+# checked once.
+_getDevice, _rawStream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+_f32 = torch.float32
 
 
-def _take(name, t, shape, dtype, device):
-    """A checked argument on `device`: `shape` and `dtype` exactly, contiguous, or None."""
-    if t is None:
-        return None
+def _check_tensor(name, t, shape, dtype, dev):
+    """Refuses a tensor that has not this shape and dtype, is not on CUDA device `dev` or not contiguous."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return
     if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
-    if t.device != device:
-        if t.is_cuda:
-            raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
-        t = t.to(device, non_blocking=True)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the other tensors on cuda:{dev}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _need(name, t, shape, dtype, device):
+def _ptr_of(name, t, shape, dtype, dev):
+    """The address of a checked argument; None stays None."""
+    if t is None:
+        return None
+    _check_tensor(name, t, shape, dtype, dev)
+    return t.data_ptr()
+
+
+def _need(name, t):
     if t is None:
         raise ValueError(f"{name} is needed")
-    return _take(name, t, shape, dtype, device)
+    return t
 
 
 def _choice(name, value, table):
@@ -332,37 +339,51 @@ def _choice(name, value, table):
     return got
 
 
-def _launch(where, fn, device, *args):
-    """Calls fn with the current stream of `device`, with that device current."""
-    i = device.index
-    if i == torch.cuda.current_device():
-        st = fn(*args, torch._C._cuda_getCurrentRawStream(i))
+def _launch(where, fn, dev, args):
+    """Calls fn with the current stream of CUDA device `dev`, with that device current."""
+    if dev == _getDevice():
+        st = fn(*args, _rawStream(dev))
     else:
-        with torch.cuda.device(i):
-            st = fn(*args, torch._C._cuda_getCurrentRawStream(i))
-    if st != _lib.GLA_OK:
+        with torch.cuda.device(dev):
+            st = fn(*args, _rawStream(dev))
+    if st:
         raise GlaError(st, where)
 
 
-def _device_of(t):
-    return t.device if t.is_cuda else torch.device("cuda", torch.cuda.current_device())
+def _from_host(fn, tensors, kw):
+    """A call on host tensors: copies to the current device, the call, copies back."""
+    device = torch.device("cuda", torch.cuda.current_device())
+    moved = [t if t is None or t.is_cuda else t.contiguous().to(device, non_blocking=True) for t in tensors]
+    kw = {k: v.to(device) if isinstance(v, torch.Tensor) and not v.is_cuda else v for k, v in kw.items()}
+    out = fn(*moved, **kw)
+    if isinstance(out, dict):
+        return dict(zip(out, _to_host(list(out.values()))))
+    if isinstance(out, tuple):
+        return tuple(_to_host(list(out)))
+    return _to_host([out])[0]
 
 
-def _buffer(name, t, nbytes, device):
-    """A workspace or saved-states buffer of the caller, checked."""
-    if t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous tensor on {device}")
+def _buffer(name, t, nbytes, dev):
+    """The address of a workspace or saved-states buffer of the caller."""
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor on cuda:{dev}")
     if t.numel() * t.element_size() < nbytes:
         raise GlaError(_lib.GLA_ERR_WORKSPACE, name)
-    return t
+    return t.data_ptr()
 
 
-def _work_buffer(workspace, nbytes, device, where):
-    if nbytes == 0:
-        raise GlaError(_lib.GLA_ERR_UNSUPPORTED, where)
-    if workspace is not None:
-        return _buffer("workspace", workspace, nbytes, device)
-    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+_descriptors = {}
+
+
+def _descriptor(key, make):
+    """The C descriptor of a problem, made once per sizes and types: (struct, reference to it)."""
+    d = _descriptors.get(key)
+    if d is None:
+        if len(_descriptors) >= 1024:
+            _descriptors.clear()
+        prob = make()
+        d = _descriptors[key] = (prob, ctypes.byref(prob))
+    return d
 
 
 def make_scan_problem(x: torch.Tensor) -> GlaProblem:
@@ -390,21 +411,21 @@ def gla_scan_fwd(x, g, h0=None, *, input: str = "plain", output_final_state: boo
     saved_states: optional device buffer (at least gla_scan_saved_bytes) that receives the states
     entering every 64 tokens, for gla_scan_bwd(..., saved_states=). Host tensors are copied to the
     current device and the results back."""
-    device = _device_of(x)
-    prob, mode, shape = make_scan_problem(x), _choice("input", input, _SCAN_INPUTS), x.shape
+    if not x.is_cuda:
+        return _from_host(gla_scan_fwd, (x, _need("g", g), h0),
+                          dict(input=input, output_final_state=output_final_state, saved_states=saved_states))
+    shape, dtype, dev = x.shape, x.dtype, x.get_device()
+    prob, ref = _descriptor((shape, dtype), lambda: make_scan_problem(x))
     ends = (shape[0], shape[1], shape[3])
-    host = not x.is_cuda
-    x = _take("x", x, shape, x.dtype, device)
-    g = _need("g", g, shape, torch.float32, device)
-    h0 = _take("h0", h0, ends, torch.float32, device)
-    if saved_states is not None:
-        _buffer("saved_states", saved_states, gla_scan_saved_bytes(prob), device)
+    mode = _choice("input", input, _SCAN_INPUTS)
+    px = _ptr_of("x", x, shape, dtype, dev)
+    pg = _ptr_of("g", _need("g", g), shape, _f32, dev)
+    ph = _ptr_of("h0", h0, ends, _f32, dev)
+    ps = None if saved_states is None else _buffer("saved_states", saved_states, gla_scan_saved_bytes(prob), dev)
     o = torch.empty_like(x)
-    hT = torch.empty(ends, dtype=torch.float32, device=device) if output_final_state else None
-    _launch("gla_scan_fwd", _lib.lib.gla_scan_fwd_save, device, ctypes.byref(prob), mode, _addr(x), _addr(g),
-            _addr(h0), _addr(o), _addr(hT), _addr(saved_states))
-    if host:
-        o, hT = _to_host([o, hT])
+    hT = g.new_empty(ends) if output_final_state else None
+    _launch("gla_scan_fwd", _lib.lib.gla_scan_fwd_save, dev,
+            (ref, mode, px, pg, ph, o.data_ptr(), None if hT is None else hT.data_ptr(), ps))
     return o, hT
 
 
@@ -415,45 +436,54 @@ def gla_scan_bwd(x, g, h0, dO, dhT=None, *, input: str = "plain", output_dh0: bo
     dh0 (fp32, or None when output_dh0 is False). saved_states: the buffer a gla_scan_fwd on the
     same x, g, h0 and input filled, or None to run the recurrence again (which needs a workspace
     of gla_scan_bwd_workspace_bytes, allocated when None)."""
-    device = _device_of(x)
-    prob, mode, shape = make_scan_problem(x), _choice("input", input, _SCAN_INPUTS), x.shape
+    if not x.is_cuda:
+        return _from_host(gla_scan_bwd, (x, _need("g", g), h0, _need("dO", dO), dhT),
+                          dict(input=input, output_dh0=output_dh0, workspace=workspace, saved_states=saved_states))
+    shape, dtype, dev = x.shape, x.dtype, x.get_device()
+    prob, ref = _descriptor((shape, dtype), lambda: make_scan_problem(x))
     ends = (shape[0], shape[1], shape[3])
-    host = not x.is_cuda
-    x = _take("x", x, shape, x.dtype, device)
-    g = _need("g", g, shape, torch.float32, device)
-    dO = _need("dO", dO, shape, x.dtype, device)
-    h0 = _take("h0", h0, ends, torch.float32, device)
-    dhT = _take("dhT", dhT, ends, torch.float32, device)
-    ws, nbytes = None, 0
+    mode = _choice("input", input, _SCAN_INPUTS)
+    px = _ptr_of("x", x, shape, dtype, dev)
+    pg = _ptr_of("g", _need("g", g), shape, _f32, dev)
+    pd = _ptr_of("dO", _need("dO", dO), shape, dtype, dev)
+    ph = _ptr_of("h0", h0, ends, _f32, dev)
+    pT = _ptr_of("dhT", dhT, ends, _f32, dev)
+    ps = pw = None
+    nbytes = 0
     if saved_states is not None:
-        _buffer("saved_states", saved_states, gla_scan_saved_bytes(prob), device)
+        ps = _buffer("saved_states", saved_states, gla_scan_saved_bytes(prob), dev)
     else:
         nbytes = gla_scan_bwd_workspace_bytes(prob)
-        ws = _work_buffer(workspace, nbytes, device, "gla_scan_bwd_workspace_bytes")
+        if nbytes == 0:
+            raise GlaError(_lib.GLA_ERR_UNSUPPORTED, "gla_scan_bwd_workspace_bytes")
+        if workspace is None:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+        pw = _buffer("workspace", workspace, nbytes, dev)
     dx, dg = torch.empty_like(x), torch.empty_like(g)
-    dh0 = torch.empty(ends, dtype=torch.float32, device=device) if output_dh0 else None
-    _launch("gla_scan_bwd", _lib.lib.gla_scan_bwd_saved, device, ctypes.byref(prob), mode, _addr(x), _addr(g),
-            _addr(h0), _addr(dO), _addr(dhT), _addr(saved_states), _addr(dx), _addr(dg), _addr(dh0), _addr(ws), nbytes)
-    if host:
-        dx, dg, dh0 = _to_host([dx, dg, dh0])
+    dh0 = g.new_empty(ends) if output_dh0 else None
+    _launch("gla_scan_bwd", _lib.lib.gla_scan_bwd_saved, dev,
+            (ref, mode, px, pg, ph, pd, pT, ps, dx.data_ptr(), dg.data_ptr(), None if dh0 is None else dh0.data_ptr(),
+             pw, nbytes))
     return {"dx": dx, "dg": dg, "dh0": dh0}
 
 
 def gla_scan_decode(x, g, state, *, input: str = "plain") -> torch.Tensor:
     """One token of gla_scan_fwd per (b, h) from `state` (fp32 [B,H,D] on the GPU, updated in
     place): x, g [B,H,1,D]. Returns o [B,H,1,D]."""
-    if not state.is_cuda or state.dtype != torch.float32 or not state.is_contiguous():
+    if not state.is_cuda or state.dtype is not _f32 or not state.is_contiguous():
         raise ValueError("state must be a contiguous float32 CUDA tensor (it is updated in place)")
-    device = state.device
-    prob, mode, shape = make_scan_problem(x), _choice("input", input, _SCAN_INPUTS), x.shape
+    if not x.is_cuda or not _need("g", g).is_cuda:
+        x, g = (t.contiguous().to(state.device, non_blocking=True) for t in (x, _need("g", g)))
+    shape, dtype, dev = x.shape, x.dtype, state.get_device()
+    _, ref = _descriptor((shape, dtype), lambda: make_scan_problem(x))
     if shape[2] != 1:
         raise ValueError("gla_scan_decode takes one token per (b, h): x must be [B, H, 1, D]")
-    x = _take("x", x, shape, x.dtype, device)
-    g = _need("g", g, shape, torch.float32, device)
-    _take("state", state, (shape[0], shape[1], shape[3]), torch.float32, device)
+    mode = _choice("input", input, _SCAN_INPUTS)
+    px = _ptr_of("x", x, shape, dtype, dev)
+    pg = _ptr_of("g", g, shape, _f32, dev)
+    ps = _ptr_of("state", state, (shape[0], shape[1], shape[3]), _f32, dev)
     o = torch.empty_like(x)
-    _launch("gla_scan_decode", _lib.lib.gla_scan_decode, device, ctypes.byref(prob), mode, x.data_ptr(), g.data_ptr(),
-            state.data_ptr(), o.data_ptr())
+    _launch("gla_scan_decode", _lib.lib.gla_scan_decode, dev, (ref, mode, px, pg, ps, o.data_ptr()))
     return o
 
 
@@ -478,21 +508,39 @@ def gla_addnorm_fwd(x, res=None, w=None, *, rscale=None, alpha: float = 1.0, kin
     None (one); kind "rms" or "layer". Returns r (res's dtype) and y (x's dtype); y is the norm of
     the fp32 sum, before r is rounded. Host tensors are copied to the current device and the
     results back."""
-    device, host, shape = _device_of(x), not x.is_cuda, x.shape
-    if res is not None and res_dtype not in (None, res.dtype):
-        raise ValueError("res_dtype is res's dtype when res is given")
-    res_dtype = res.dtype if res is not None else (res_dtype or x.dtype)
-    prob = _addnorm_problem(x, res_dtype, kind, eps, alpha)
-    x = _take("x", x, shape, x.dtype, device)
-    res = _take("res", res, shape, res_dtype, device)
-    w = _take("w", w, shape[-1:], torch.float32, device)
-    rscale = _take("rscale", rscale, shape[-1:], torch.float32, device)
-    r, y = torch.empty(shape, dtype=res_dtype, device=device), torch.empty_like(x)
-    _launch("gla_addnorm_fwd", _lib.lib.gla_addnorm_fwd, device, ctypes.byref(prob), _addr(x), _addr(res),
-            _addr(rscale), _addr(w), _addr(r), _addr(y))
-    if host:
-        r, y = _to_host([r, y])
+    if not x.is_cuda:
+        return _from_host(gla_addnorm_fwd, (x, res, w),
+                          dict(rscale=rscale, alpha=alpha, kind=kind, eps=eps, res_dtype=res_dtype))
+    shape, dtype, dev = x.shape, x.dtype, x.get_device()
+    if res is not None:
+        if res_dtype not in (None, res.dtype):
+            raise ValueError("res_dtype is res's dtype when res is given")
+        res_dtype = res.dtype
+    elif res_dtype is None:
+        res_dtype = dtype
+    _, ref = _descriptor((shape, dtype, res_dtype, kind, eps, alpha),
+                         lambda: _addnorm_problem(x, res_dtype, kind, eps, alpha))
+    cols = shape[-1:]
+    px = _ptr_of("x", x, shape, dtype, dev)
+    pr = _ptr_of("res", res, shape, res_dtype, dev)
+    pw = _ptr_of("w", w, cols, _f32, dev)
+    ps = _ptr_of("rscale", rscale, cols, _f32, dev)
+    y = torch.empty_like(x)
+    r = torch.empty_like(x) if res_dtype is dtype else torch.empty_like(x, dtype=res_dtype)
+    _launch("gla_addnorm_fwd", _lib.lib.gla_addnorm_fwd, dev, (ref, px, pr, ps, pw, r.data_ptr(), y.data_ptr()))
     return r, y
+
+
+def _partials(name, workspace, nbytes, dev, like):
+    """(address, bytes) of the workspace for the partial rows of column sums; none is needed where a single
+    block writes them (256 bytes or less)."""
+    if nbytes == 0:
+        raise GlaError(_lib.GLA_ERR_UNSUPPORTED, name)
+    if workspace is None:
+        if nbytes <= 256:
+            return None, None, 0
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    return workspace, _buffer("workspace", workspace, nbytes, dev), nbytes
 
 
 def gla_addnorm_bwd(x, r, w, dy, dr=None, *, rscale=None, alpha: float = 1.0, kind: str = "rms", eps: float = 1e-6,
@@ -503,28 +551,32 @@ def gla_addnorm_bwd(x, r, w, dy, dr=None, *, rscale=None, alpha: float = 1.0, ki
     dtype it equals dres), dw (fp32 [D], None without w) and drscale (fp32 [D], None without
     rscale). x is only read for drscale and may be None without rscale; dr [..., D] is the
     gradient that reaches r from later blocks, or None."""
-    device, host, shape = _device_of(dy), not dy.is_cuda, dy.shape
-    prob = _addnorm_problem(dy, r.dtype, kind, eps, alpha)
-    D = shape[-1:]
-    dy = _take("dy", dy, shape, dy.dtype, device)
-    r = _take("r", r, shape, r.dtype, device)
-    dr = _take("dr", dr, shape, r.dtype, device)
-    w = _take("w", w, D, torch.float32, device)
-    rscale = _take("rscale", rscale, D, torch.float32, device)
-    x = _need("x (for rscale's gradient)", x, shape, dy.dtype, device) if rscale is not None else None
-    nbytes = _lib.lib.gla_addnorm_workspace_bytes(ctypes.byref(prob))
-    ws = _work_buffer(workspace, nbytes, device, "gla_addnorm_workspace_bytes")
+    if not dy.is_cuda:
+        return _from_host(gla_addnorm_bwd, (x, r, w, dy, dr),
+                          dict(rscale=rscale, alpha=alpha, kind=kind, eps=eps, output_dx=output_dx,
+                               workspace=workspace))
+    shape, dtype, dev, res_dtype = dy.shape, dy.dtype, dy.get_device(), r.dtype
+    _, ref = _descriptor((shape, dtype, res_dtype, kind, eps, alpha),
+                         lambda: _addnorm_problem(dy, res_dtype, kind, eps, alpha))
+    cols = shape[-1:]
+    pdy = _ptr_of("dy", dy, shape, dtype, dev)
+    pr = _ptr_of("r", r, shape, res_dtype, dev)
+    pdr = _ptr_of("dr", dr, shape, res_dtype, dev)
+    pw = _ptr_of("w", w, cols, _f32, dev)
+    px = ps = ds = None
+    if rscale is not None:
+        ps = _ptr_of("rscale", rscale, cols, _f32, dev)
+        px = _ptr_of("x (for rscale's gradient)", _need("x (for rscale's gradient)", x), shape, dtype, dev)
+        ds = torch.empty_like(rscale)
+    ws, pws, nbytes = _partials("gla_addnorm_workspace_bytes", workspace, _lib.lib.gla_addnorm_workspace_bytes(ref), dev,
+                                dy)
     dres = torch.empty_like(r)
     dx = torch.empty_like(dy) if output_dx else None
     dw = torch.empty_like(w) if w is not None else None
-    ds = torch.empty_like(rscale) if rscale is not None else None
-    _launch("gla_addnorm_bwd", _lib.lib.gla_addnorm_bwd, device, ctypes.byref(prob), _addr(x), _addr(r),
-            _addr(rscale), _addr(w), _addr(dy), _addr(dr), _addr(dres), _addr(dx), _addr(dw), _addr(ds), _addr(ws),
-            nbytes)
-    out = {"dres": dres, "dx": dx, "dw": dw, "drscale": ds}
-    if host:
-        out = dict(zip(out, _to_host(list(out.values()))))
-    return out
+    _launch("gla_addnorm_bwd", _lib.lib.gla_addnorm_bwd, dev,
+            (ref, px, pr, ps, pw, pdy, pdr, dres.data_ptr(), None if dx is None else dx.data_ptr(),
+             None if dw is None else dw.data_ptr(), None if ds is None else ds.data_ptr(), pws, nbytes))
+    return {"dres": dres, "dx": dx, "dw": dw, "drscale": ds}
 
 
 def _headnorm_problem(o, w, act, kind, eps) -> GlaNormProblem:
@@ -542,17 +594,18 @@ def gla_headnorm_fwd(o, z=None, w=None, *, act: str = "silu", kind: str = "rms",
     act ("silu" or "sigmoid"), None: no gate; w fp32 [D] (shared by the heads) or [H,D], None: one;
     kind "rms" or "layer". Returns y [B,L,H,D]: y.view(B, L, H * D) is the out-projection's input.
     Host tensors are copied to the current device and the result back."""
-    device, host = _device_of(o), not o.is_cuda
-    prob = _headnorm_problem(o, w, act, kind, eps)
-    B, H, L, D = o.shape
-    o = _take("o", o, o.shape, o.dtype, device)
-    z = _take("z", z, (B, L, H, D), o.dtype, device)
-    w = _take("w", w, (H, D) if prob.w_per_head else (D,), torch.float32, device)
-    y = torch.empty((B, L, H, D), dtype=o.dtype, device=device)
-    _launch("gla_headnorm_fwd", _lib.lib.gla_headnorm_fwd, device, ctypes.byref(prob), _addr(o), _addr(z), _addr(w),
-            _addr(y))
-    if host:
-        (y,) = _to_host([y])
+    if not o.is_cuda:
+        return _from_host(gla_headnorm_fwd, (o, z, w), dict(act=act, kind=kind, eps=eps))
+    shape, dtype, dev = o.shape, o.dtype, o.get_device()
+    heads = w is not None and w.dim() == 2
+    _, ref = _descriptor((shape, dtype, heads, act, kind, eps), lambda: _headnorm_problem(o, w, act, kind, eps))
+    B, H, L, D = shape
+    tokens = (B, L, H, D)
+    po = _ptr_of("o", o, shape, dtype, dev)
+    pz = _ptr_of("z", z, tokens, dtype, dev)
+    pw = _ptr_of("w", w, (H, D) if heads else (D,), _f32, dev)
+    y = o.new_empty(tokens)
+    _launch("gla_headnorm_fwd", _lib.lib.gla_headnorm_fwd, dev, (ref, po, pz, pw, y.data_ptr()))
     return y
 
 
@@ -560,24 +613,27 @@ def gla_headnorm_bwd(o, z, w, dy, *, act: str = "silu", kind: str = "rms", eps: 
                      workspace: Optional[torch.Tensor] = None) -> Dict[str, Optional[torch.Tensor]]:
     """Gradients of sum(dy * y) of gla_headnorm_fwd: dict do [B,H,L,D], dz [B,L,H,D] (None without
     z), dw (fp32, shaped like w; None without w)."""
-    device, host = _device_of(o), not o.is_cuda
-    prob = _headnorm_problem(o, w, act, kind, eps)
-    B, H, L, D = o.shape
-    o = _take("o", o, o.shape, o.dtype, device)
-    z = _take("z", z, (B, L, H, D), o.dtype, device)
-    dy = _need("dy", dy, (B, L, H, D), o.dtype, device)
-    w = _take("w", w, (H, D) if prob.w_per_head else (D,), torch.float32, device)
-    nbytes = _lib.lib.gla_headnorm_workspace_bytes(ctypes.byref(prob))
-    ws = _work_buffer(workspace, nbytes, device, "gla_headnorm_workspace_bytes")
+    if not o.is_cuda:
+        return _from_host(gla_headnorm_bwd, (o, z, w, _need("dy", dy)),
+                          dict(act=act, kind=kind, eps=eps, workspace=workspace))
+    shape, dtype, dev = o.shape, o.dtype, o.get_device()
+    heads = w is not None and w.dim() == 2
+    _, ref = _descriptor((shape, dtype, heads, act, kind, eps), lambda: _headnorm_problem(o, w, act, kind, eps))
+    B, H, L, D = shape
+    tokens = (B, L, H, D)
+    po = _ptr_of("o", o, shape, dtype, dev)
+    pz = _ptr_of("z", z, tokens, dtype, dev)
+    pdy = _ptr_of("dy", _need("dy", dy), tokens, dtype, dev)
+    pw = _ptr_of("w", w, (H, D) if heads else (D,), _f32, dev)
+    ws, pws, nbytes = _partials("gla_headnorm_workspace_bytes", workspace, _lib.lib.gla_headnorm_workspace_bytes(ref),
+                                dev, o)
     d_o = torch.empty_like(o)
     dz = torch.empty_like(z) if z is not None else None
     dw = torch.empty_like(w) if w is not None else None
-    _launch("gla_headnorm_bwd", _lib.lib.gla_headnorm_bwd, device, ctypes.byref(prob), _addr(o), _addr(z), _addr(w),
-            _addr(dy), _addr(d_o), _addr(dz), _addr(dw), _addr(ws), nbytes)
-    out = {"do": d_o, "dz": dz, "dw": dw}
-    if host:
-        out = dict(zip(out, _to_host(list(out.values()))))
-    return out
+    _launch("gla_headnorm_bwd", _lib.lib.gla_headnorm_bwd, dev,
+            (ref, po, pz, pw, pdy, d_o.data_ptr(), None if dz is None else dz.data_ptr(),
+             None if dw is None else dw.data_ptr(), pws, nbytes))
+    return {"do": d_o, "dz": dz, "dw": dw}
 
 
 def gla_shard_state(k, v, g=None, igate=None, *, chunk: int = 64) -> Tuple[torch.Tensor, torch.Tensor]:

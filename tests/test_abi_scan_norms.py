@@ -175,10 +175,13 @@ def test_norms_refuse_arguments():
 
 
 def test_norm_workspace_holds_a_partial_row_per_block():
-    """Never more partial rows than rows, and at least one row each for dw and drscale."""
+    """Never more partial rows than rows, and at least two each for dw and drscale where several blocks run; a
+    single block writes the sums itself and needs none."""
     for D in (1, 72, 100, 4096, 16384):
         one = lib.gla_addnorm_workspace_bytes(ctypes.byref(nprob(B=1, L=1, D=D)))
         many = lib.gla_addnorm_workspace_bytes(ctypes.byref(nprob(B=8, L=8192, D=D)))
-        assert 8 * D <= one <= many < 1 << 28
+        assert one == 256 and 256 + 16 * D <= many < 1 << 28
         head = lib.gla_headnorm_workspace_bytes(ctypes.byref(nprob(B=8, L=8192, D=D, H=16)))
         assert 4 * D * 16 <= head < 1 << 28
+        assert lib.gla_headnorm_workspace_bytes(ctypes.byref(nprob(B=1, L=1, D=D, H=16, w_per_head=1))) == 256
+        assert lib.gla_headnorm_workspace_bytes(ctypes.byref(nprob(B=1, L=1, D=D, H=16))) >= 256 + 4 * 16 * D

@@ -312,6 +312,21 @@ def test_row_sums_repeat_bit_for_bit():
             assert torch.equal(p[n], q[n]), n
 
 
+def test_few_rows_need_no_workspace():
+    """One block's column sums are the result: no workspace, nothing else launched."""
+    from linear_rnn_b200 import _lib, ops
+    x, r0, w, rs, dy, dr = cuda(*addnorm_inputs(3, 64, "bf16", "bf16", 76))
+    n0 = _lib.launch_count()
+    g = ops.gla_addnorm_bwd(x, r0, w, dy, dr, rscale=rs, eps=EPS)
+    assert _lib.launch_count() == n0 + 1
+    ref = norms.addnorm_bwd(f64(x), f64(r0), f64(rs), f64(w), f64(dy), f64(dr), 1.0, "rms", EPS)
+    for n in ("dw", "drscale"):
+        within(g[n], ref[n], 1e-5 * np.abs(ref[n]).max(), n)
+    check_headnorm(1, 6, 2, 64, "f32", "layer", "silu", True, True, True, 77)    # one block per head, its own weights
+    check_headnorm(1, 1, 2, 64, "f32", "layer", "silu", False, True, True, 78)
+    check_headnorm(1, 6, 2, 64, "f32", "layer", "silu", False, True, True, 79)   # heads share them: summed
+
+
 def test_many_rows():
     """More rows than any grid: every block walks several, and the sums over rows are long (their tolerance
     counts the additions that follow one another: rows over blocks and groups, here below 200 in all)."""
