@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 && VEC == 8 ? 2 : 1024 / MAX
 }
 
 template <typename T, typename R, int VEC, int NV, int S, int KIND, int MAXT>
-__global__ void __launch_bounds__(MAXT < 512 ? 512 : MAXT)   // 16384 x 2048: 79 us; bounded by 256 threads, 2 blocks 88
+__global__ void __launch_bounds__(MAXT < 512 ? 448 : MAXT)   // 144 registers. 16384 x 2048: 78 us; 81 at 512 threads' 128
     k_addnorm_bwd(const T* __restrict__ x, const R* __restrict__ r_in, const float* __restrict__ rscale,
                   const float* __restrict__ w, const T* __restrict__ dy, const R* dr, R* dres, T* __restrict__ dx,
                   float* __restrict__ pdw, float* __restrict__ pds, int rows, int D, int G, float alpha, float eps) {
