@@ -12,29 +12,35 @@ using namespace norm;
 
 // Blocks of 256 threads per SM that the registers leave room for, 16384 x 4096: 4 with an fp32 residual (2: 139 us,
 // 3: 143, 4: 135), 2 with everything in bf16 (2: 100 us, 3: 104, 4: 105).
-template <typename T, typename R, int VEC, int NV, int S, int KIND, int MAXT>
-__global__ void __launch_bounds__(MAXT, MAXT == 256 && VEC == 8 ? 2 : 1024 / MAXT)
+template <typename T, typename R, int VEC, int NV, int S, int KIND, int MAXT, bool ODD>
+__global__ void __launch_bounds__(MAXT, ODD || (MAXT == 256 && VEC == 8) ? (MAXT == 256 ? 2 : 1) : 1024 / MAXT)
     k_addnorm_fwd(const T* __restrict__ x, const R* res, const float* __restrict__ rscale,
                   const float* __restrict__ w, R* r_out, T* __restrict__ y, int rows, int D, int G, float alpha,
                   float eps) {
     extern __shared__ __align__(128) uint8_t smem[];
     constexpr int NP = kPairs<VEC>;
-    using F = Feed<S>;
+    using F = std::conditional_t<ODD, RowFeed<S>, Feed<S>>;
     constexpr int XOFF = F::template bytes<R, VEC, NV>();   // res first, then x
     constexpr int ROW = XOFF + F::template bytes<T, VEC, NV>();
     RowSum sum{reinterpret_cast<float*>(smem), G, 0};
-    F feed{smem + kHead + 16 * threadIdx.x, ROW * (int)blockDim.x, 0};
+    F feed = make_feed<S, ODD>(smem + kHead, ROW, G);
     const int grp = threadIdx.x / G, ngrp = blockDim.x / G;
-    const Place P{(int)threadIdx.x - grp * G, G, D / VEC};
+    const Place P{(int)threadIdx.x - grp * G, G, ODD ? (D + 1) / 2 : D / VEC, D};
     const float inv_d = 1.f / D;
     uint64_t wv[NV][NP], sv[NV][NP];   // this thread's columns of w and alpha rscale
-    load_columns<VEC, NV>(wv, w, P, 1.f);
-    load_columns<VEC, NV>(sv, rscale, P, alpha);
+    load_columns<VEC, NV, ODD>(wv, w, P, 1.f);
+    load_columns<VEC, NV, ODD>(sv, rscale, P, alpha);
     const long long step = (long long)gridDim.x * ngrp;
     long long row = (long long)blockIdx.x * ngrp + grp;
     auto copy = [&](long long to, int stage) {
         if constexpr (S > 0) {
-            if (to < rows)
+            if constexpr (ODD) {
+                if (to < rows) {
+                    const size_t e0 = (size_t)to * D, n = (size_t)rows * D;
+                    if (res) feed.copy_row(stage, 0, res, e0, n, P);
+                    feed.copy_row(stage, XOFF, x, e0, n, P);
+                }
+            } else if (to < rows) {
 #pragma unroll
                 for (int j = 0; j < NV; ++j)
                     if (P.has(j)) {
@@ -42,6 +48,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 && VEC == 8 ? 2 : 1024 / MAX
                         if (res) feed.template copy<R, VEC>(stage, 0, j, res + c);
                         feed.template copy<T, VEC>(stage, XOFF, j, x + c);
                     }
+            }
             feed.commit();
         }
     };
@@ -75,8 +82,8 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 && VEC == 8 ? 2 : 1024 / MAX
             if (live && P.has(j)) {
                 uint64_t xv[NP];
                 if constexpr (S > 0) {
-                    feed.template read<T, VEC>(XOFF, j, xv);
-                    if (res) feed.template read<R, VEC>(0, j, r[j]);
+                    feed.template read<T, VEC>(XOFF, j, xv, off, P);
+                    if (res) feed.template read<R, VEC>(0, j, r[j], off, P);
                 } else if constexpr (kHold<S, NV>) {
 #pragma unroll
                     for (int i = 0; i < NP; ++i) xv[i] = xn[j][i], r[j][i] = rn[j][i];
@@ -86,11 +93,11 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 && VEC == 8 ? 2 : 1024 / MAX
                 }
 #pragma unroll
                 for (int i = 0; i < NP; ++i) r[j][i] = f2_fma(sv[j][i], xv[i], r[j][i]);
-                if (r_out) store_piece<VEC>(r_out + off + P.col<VEC>(j), r[j]);
+                if (r_out) put_piece<VEC, ODD>(r_out + off, P, j, r[j]);
             }
         }
         hold(row + step);
-        center<KIND, VEC, NV>(sum, r, P, inv_d);
+        center<KIND, VEC, NV, ODD>(sum, r, P, inv_d);
         float s[1] = {square_sum<VEC, NV>(r)};
         sum(s);
         const uint64_t rstd = f2_all(rsqrtf(fmaf(s[0], inv_d, eps)));
@@ -99,35 +106,43 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 && VEC == 8 ? 2 : 1024 / MAX
             if (live && P.has(j)) {
 #pragma unroll
                 for (int i = 0; i < NP; ++i) r[j][i] = f2_mul(f2_mul(r[j][i], rstd), wv[j][i]);
-                store_piece<VEC>(y + off + P.col<VEC>(j), r[j]);
+                put_piece<VEC, ODD>(y + off, P, j, r[j]);
             }
         feed.next();
     }
 }
 
-template <typename T, typename R, int VEC, int NV, int S, int KIND, int MAXT>
+template <typename T, typename R, int VEC, int NV, int S, int KIND, int MAXT, bool ODD>
 __global__ void __launch_bounds__(MAXT < 512 ? 448 : MAXT)   // 144 registers. 16384 x 2048: 78 us; 81 at 512 threads' 128
     k_addnorm_bwd(const T* __restrict__ x, const R* __restrict__ r_in, const float* __restrict__ rscale,
                   const float* __restrict__ w, const T* __restrict__ dy, const R* dr, R* dres, T* __restrict__ dx,
                   float* __restrict__ pdw, float* __restrict__ pds, int rows, int D, int G, float alpha, float eps) {
     extern __shared__ __align__(128) uint8_t smem[];
     constexpr int NP = kPairs<VEC>;
-    using F = Feed<S>;
+    using F = std::conditional_t<ODD, RowFeed<S>, Feed<S>>;
     constexpr int BR = F::template bytes<R, VEC, NV>(), BT = F::template bytes<T, VEC, NV>();
     constexpr int DROFF = BR, DYOFF = 2 * BR, XOFF = 2 * BR + BT, ROW = 2 * (BR + BT);   // r, dr, dy, x
     RowSum sum{reinterpret_cast<float*>(smem), G, 0};
-    F feed{smem + kHead + 16 * threadIdx.x, ROW * (int)blockDim.x, 0};
+    F feed = make_feed<S, ODD>(smem + kHead, ROW, G);
     const int grp = threadIdx.x / G, ngrp = blockDim.x / G;
-    const Place P{(int)threadIdx.x - grp * G, G, D / VEC};
+    const Place P{(int)threadIdx.x - grp * G, G, ODD ? (D + 1) / 2 : D / VEC, D};
     const float inv_d = 1.f / D;
     uint64_t wv[NV][NP], sv[NV][NP], aw[NV][NP] = {}, as[NV][NP] = {};
-    load_columns<VEC, NV>(wv, w, P, 1.f);
-    load_columns<VEC, NV>(sv, rscale, P, alpha);
+    load_columns<VEC, NV, ODD>(wv, w, P, 1.f);
+    load_columns<VEC, NV, ODD>(sv, rscale, P, alpha);
     const long long step = (long long)gridDim.x * ngrp;
     long long row = (long long)blockIdx.x * ngrp + grp;
     auto copy = [&](long long to, int stage) {
         if constexpr (S > 0) {
-            if (to < rows)
+            if constexpr (ODD) {
+                if (to < rows) {
+                    const size_t e0 = (size_t)to * D, n = (size_t)rows * D;
+                    feed.copy_row(stage, 0, r_in, e0, n, P);
+                    feed.copy_row(stage, DYOFF, dy, e0, n, P);
+                    if (dr) feed.copy_row(stage, DROFF, dr, e0, n, P);
+                    if (pds) feed.copy_row(stage, XOFF, x, e0, n, P);
+                }
+            } else if (to < rows) {
 #pragma unroll
                 for (int j = 0; j < NV; ++j)
                     if (P.has(j)) {
@@ -137,6 +152,7 @@ __global__ void __launch_bounds__(MAXT < 512 ? 448 : MAXT)   // 144 registers. 1
                         if (dr) feed.template copy<R, VEC>(stage, DROFF, j, dr + c);
                         if (pds) feed.template copy<T, VEC>(stage, XOFF, j, x + c);
                     }
+            }
             feed.commit();
         }
     };
@@ -174,8 +190,8 @@ __global__ void __launch_bounds__(MAXT < 512 ? 448 : MAXT)   // 144 registers. 1
             for (int i = 0; i < NP; ++i) r[j][i] = d[j][i] = 0;
             if (live && P.has(j)) {
                 if constexpr (S > 0) {
-                    feed.template read<R, VEC>(0, j, r[j]);
-                    feed.template read<T, VEC>(DYOFF, j, d[j]);
+                    feed.template read<R, VEC>(0, j, r[j], off, P);
+                    feed.template read<T, VEC>(DYOFF, j, d[j], off, P);
                 } else if constexpr (kHold<S, NV>) {
 #pragma unroll
                     for (int i = 0; i < NP; ++i) r[j][i] = rn[j][i], d[j][i] = dn[j][i];
@@ -186,7 +202,7 @@ __global__ void __launch_bounds__(MAXT < 512 ? 448 : MAXT)   // 144 registers. 1
             }
         }
         hold(row + step);
-        center<KIND, VEC, NV>(sum, r, P, inv_d);
+        center<KIND, VEC, NV, ODD>(sum, r, P, inv_d);
         // sums of (r - mu)^2, d (r - mu) and, for the layer norm, d
         uint64_t t0 = 0, t1 = 0, t2 = 0;
 #pragma unroll
@@ -216,7 +232,7 @@ __global__ void __launch_bounds__(MAXT < 512 ? 448 : MAXT)   // 144 registers. 1
                 for (int i = 0; i < NP; ++i) t[i] = 0;
                 if (dr) {
                     if constexpr (S > 0) {
-                        feed.template read<R, VEC>(DROFF, j, t);
+                        feed.template read<R, VEC>(DROFF, j, t, off, P);
                     } else if constexpr (kHold<S, NV>) {
 #pragma unroll
                         for (int i = 0; i < NP; ++i) t[i] = drc[j][i];
@@ -232,10 +248,10 @@ __global__ void __launch_bounds__(MAXT < 512 ? 448 : MAXT)   // 144 registers. 1
                     if (KIND == GLA_NORM_LAYER) t[i] = f2_add(t[i], md);
                     t[i] = f2_fma(f2_mul(d[j][i], wv[j][i]), rstd2, t[i]);
                 }
-                if (dres) store_piece<VEC>(dres + off + P.col<VEC>(j), t);
+                if (dres) put_piece<VEC, ODD>(dres + off, P, j, t);
                 if (pds) {
                     if constexpr (S > 0) {
-                        feed.template read<T, VEC>(XOFF, j, xv);
+                        feed.template read<T, VEC>(XOFF, j, xv, off, P);
                     } else if constexpr (kHold<S, NV>) {
 #pragma unroll
                         for (int i = 0; i < NP; ++i) xv[i] = xc[j][i];
@@ -248,20 +264,20 @@ __global__ void __launch_bounds__(MAXT < 512 ? 448 : MAXT)   // 144 registers. 1
                 if (dx) {
 #pragma unroll
                     for (int i = 0; i < NP; ++i) t[i] = f2_mul(t[i], sv[j][i]);
-                    store_piece<VEC>(dx + off + P.col<VEC>(j), t);
+                    put_piece<VEC, ODD>(dx + off, P, j, t);
                 }
             }
         feed.next();
     }
     grid_dep_launch();
     float* cols = reinterpret_cast<float*>(smem);
-    if (pdw) write_partial<VEC, NV>(aw, cols, grp, P, pdw + (size_t)blockIdx.x * D);
+    if (pdw) write_partial<VEC, NV, ODD>(aw, cols, grp, P, pdw + (size_t)blockIdx.x * D);
     if (pds) {
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
             for (int i = 0; i < NP; ++i) as[j][i] = f2_mul(as[j][i], f2_all(alpha));
-        write_partial<VEC, NV>(as, cols, grp, P, pds + (size_t)blockIdx.x * D);
+        write_partial<VEC, NV, ODD>(as, cols, grp, P, pds + (size_t)blockIdx.x * D);
     }
 }
 
@@ -316,7 +332,7 @@ gla_status gla_addnorm_fwd(const gla_norm_problem* p, const void* x, const void*
         return by_shape<sizeof(T) + sizeof(R) == 4, sizeof(T) == 4>(rp, stages, [&](auto sh) {
             return by_kind(p->kind, [&](auto kind) {
                 using Sh = decltype(sh);
-                auto kern = k_addnorm_fwd<T, R, Sh::vec, Sh::nv, Sh::stages, decltype(kind)::value, Sh::maxt>;
+                auto kern = k_addnorm_fwd<T, R, Sh::vec, Sh::nv, Sh::stages, decltype(kind)::value, Sh::maxt, Sh::odd>;
                 const size_t smem = block_smem(rp, Sh::stages, thread_bytes);
                 static std::atomic<bool> seen[kMaxDevices];
                 static Occupancy known;
@@ -363,7 +379,7 @@ gla_status gla_addnorm_bwd(const gla_norm_problem* p, const void* x, const void*
             return by_shape<sizeof(T) + sizeof(R) == 4, sizeof(T) == 4>(rp, stages, [&](auto sh) {
                 return by_kind(p->kind, [&](auto kind) {
                     using Sh = decltype(sh);
-                    auto kern = k_addnorm_bwd<T, R, Sh::vec, Sh::nv, Sh::stages, decltype(kind)::value, Sh::maxt>;
+                    auto kern = k_addnorm_bwd<T, R, Sh::vec, Sh::nv, Sh::stages, decltype(kind)::value, Sh::maxt, Sh::odd>;
                     const size_t smem = block_smem(rp, Sh::stages, thread_bytes);
                     static std::atomic<bool> seen[kMaxDevices];
                 static Occupancy known;

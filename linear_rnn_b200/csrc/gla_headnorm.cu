@@ -74,34 +74,41 @@ struct Walk {
 };
 
 // blockIdx.y = head; a row of the block = one token of that head.
-template <typename T, int VEC, int NV, int S, int KIND, int ACT, int MAXT>
+template <typename T, int VEC, int NV, int S, int KIND, int ACT, int MAXT, bool ODD>
 __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1)   // 68 us at 128 registers, 77 at 64
     k_headnorm_fwd(const T* __restrict__ o, const T* __restrict__ z, const float* __restrict__ w, T* __restrict__ y,
                    int tokens, int H, int L, int D, int G, int w_stride, float eps) {
     extern __shared__ __align__(128) uint8_t smem[];
     constexpr int NP = kPairs<VEC>;
-    using F = Feed<S>;
+    using F = std::conditional_t<ODD, RowFeed<S>, Feed<S>>;
     constexpr int ZOFF = F::template bytes<T, VEC, NV>(), ROW = 2 * ZOFF;
     RowSum sum{reinterpret_cast<float*>(smem), G, 0};
-    F feed{smem + kHead + 16 * threadIdx.x, ROW * (int)blockDim.x, 0};
+    F feed = make_feed<S, ODD>(smem + kHead, ROW, G);
     const int grp = threadIdx.x / G, ngrp = blockDim.x / G, h = blockIdx.y;
-    const Place P{(int)threadIdx.x - grp * G, G, D / VEC};
+    const Place P{(int)threadIdx.x - grp * G, G, ODD ? (D + 1) / 2 : D / VEC, D};
     const float inv_d = 1.f / D;
     uint64_t wv[NV][NP];
-    load_columns<VEC, NV>(wv, w ? w + (size_t)h * w_stride : nullptr, P, 1.f);
+    load_columns<VEC, NV, ODD>(wv, w ? w + (size_t)h * w_stride : nullptr, P, 1.f);
     const long long step = (long long)gridDim.x * ngrp;
     long long t = (long long)blockIdx.x * ngrp + grp, ahead = t;
     const Walk walk(step, H, L, D);
     Token in = walk.first(t, h, H, D), out = in;   // the next token to copy, the current one
     auto copy = [&](int stage) {
         if constexpr (S > 0) {
-            if (ahead < tokens)
+            if constexpr (ODD) {
+                if (ahead < tokens) {
+                    const size_t n = (size_t)tokens * H * D;
+                    feed.copy_row(stage, 0, o, in.src, n, P);
+                    if (z) feed.copy_row(stage, ZOFF, z, in.dst, n, P);
+                }
+            } else if (ahead < tokens) {
 #pragma unroll
                 for (int j = 0; j < NV; ++j)
                     if (P.has(j)) {
                         feed.template copy<T, VEC>(stage, 0, j, o + in.src + P.col<VEC>(j));
                         if (z) feed.template copy<T, VEC>(stage, ZOFF, j, z + in.dst + P.col<VEC>(j));
                     }
+            }
             feed.commit();
             walk.go(in);
             ahead += step;
@@ -121,11 +128,11 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1)   // 68 us at 128 r
 #pragma unroll
             for (int i = 0; i < NP; ++i) r[j][i] = 0;
             if (live && P.has(j)) {
-                if constexpr (S > 0) feed.template read<T, VEC>(0, j, r[j]);
+                if constexpr (S > 0) feed.template read<T, VEC>(0, j, r[j], out.src, P);
                 else load_piece<VEC>(o + out.src + P.col<VEC>(j), r[j]);
             }
         }
-        center<KIND, VEC, NV>(sum, r, P, inv_d);
+        center<KIND, VEC, NV, ODD>(sum, r, P, inv_d);
         float s[1] = {square_sum<VEC, NV>(r)};
         sum(s);
         const uint64_t rstd = f2_all(rsqrtf(fmaf(s[0], inv_d, eps)));
@@ -136,7 +143,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1)   // 68 us at 128 r
                 for (int i = 0; i < NP; ++i) r[j][i] = f2_mul(f2_mul(r[j][i], rstd), wv[j][i]);
                 if (z) {
                     uint64_t zv[NP];
-                    if constexpr (S > 0) feed.template read<T, VEC>(ZOFF, j, zv);
+                    if constexpr (S > 0) feed.template read<T, VEC>(ZOFF, j, zv, out.dst, P);
                     else load_piece<VEC>(z + out.dst + P.col<VEC>(j), zv);
 #pragma unroll
                     for (int i = 0; i < NP; ++i) {
@@ -145,36 +152,43 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1)   // 68 us at 128 r
                         r[j][i] = f2_mul(r[j][i], f);
                     }
                 }
-                store_piece<VEC>(y + out.dst + P.col<VEC>(j), r[j]);
+                put_piece<VEC, ODD>(y + out.dst, P, j, r[j]);
             }
         feed.next();
         walk.go(out);
     }
 }
 
-template <typename T, int VEC, int NV, int S, int KIND, int ACT, int MAXT>
+template <typename T, int VEC, int NV, int S, int KIND, int ACT, int MAXT, bool ODD>
 __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1)
     k_headnorm_bwd(const T* __restrict__ o, const T* __restrict__ z, const float* __restrict__ w,
                    const T* __restrict__ dy, T* __restrict__ d_o, T* __restrict__ dz, float* __restrict__ pdw,
                    int tokens, int H, int L, int D, int G, int w_stride, float eps) {
     extern __shared__ __align__(128) uint8_t smem[];
     constexpr int NP = kPairs<VEC>;
-    using F = Feed<S>;
+    using F = std::conditional_t<ODD, RowFeed<S>, Feed<S>>;
     constexpr int ZOFF = F::template bytes<T, VEC, NV>(), YOFF = 2 * ZOFF, ROW = 3 * ZOFF;
     RowSum sum{reinterpret_cast<float*>(smem), G, 0};
-    F feed{smem + kHead + 16 * threadIdx.x, ROW * (int)blockDim.x, 0};
+    F feed = make_feed<S, ODD>(smem + kHead, ROW, G);
     const int grp = threadIdx.x / G, ngrp = blockDim.x / G, h = blockIdx.y;
-    const Place P{(int)threadIdx.x - grp * G, G, D / VEC};
+    const Place P{(int)threadIdx.x - grp * G, G, ODD ? (D + 1) / 2 : D / VEC, D};
     const float inv_d = 1.f / D;
     uint64_t wv[NV][NP], aw[NV][NP] = {};
-    load_columns<VEC, NV>(wv, w ? w + (size_t)h * w_stride : nullptr, P, 1.f);
+    load_columns<VEC, NV, ODD>(wv, w ? w + (size_t)h * w_stride : nullptr, P, 1.f);
     const long long step = (long long)gridDim.x * ngrp;
     long long t = (long long)blockIdx.x * ngrp + grp, ahead = t;
     const Walk walk(step, H, L, D);
     Token in = walk.first(t, h, H, D), out = in;   // the next token to copy, the current one
     auto copy = [&](int stage) {
         if constexpr (S > 0) {
-            if (ahead < tokens)
+            if constexpr (ODD) {
+                if (ahead < tokens) {
+                    const size_t n = (size_t)tokens * H * D;
+                    feed.copy_row(stage, 0, o, in.src, n, P);
+                    feed.copy_row(stage, YOFF, dy, in.dst, n, P);
+                    if (z) feed.copy_row(stage, ZOFF, z, in.dst, n, P);
+                }
+            } else if (ahead < tokens) {
 #pragma unroll
                 for (int j = 0; j < NV; ++j)
                     if (P.has(j)) {
@@ -182,6 +196,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1)
                         feed.template copy<T, VEC>(stage, YOFF, j, dy + in.dst + P.col<VEC>(j));
                         if (z) feed.template copy<T, VEC>(stage, ZOFF, j, z + in.dst + P.col<VEC>(j));
                     }
+            }
             feed.commit();
             walk.go(in);
             ahead += step;
@@ -201,11 +216,11 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1)
 #pragma unroll
             for (int i = 0; i < NP; ++i) r[j][i] = 0;
             if (live && P.has(j)) {
-                if constexpr (S > 0) feed.template read<T, VEC>(0, j, r[j]);
+                if constexpr (S > 0) feed.template read<T, VEC>(0, j, r[j], out.src, P);
                 else load_piece<VEC>(o + out.src + P.col<VEC>(j), r[j]);
             }
         }
-        center<KIND, VEC, NV>(sum, r, P, inv_d);
+        center<KIND, VEC, NV, ODD>(sum, r, P, inv_d);
         uint64_t t0 = 0, t1 = 0, t2 = 0;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
@@ -213,10 +228,10 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1)
             for (int i = 0; i < NP; ++i) q[j][i] = d[j][i] = 0;
             if (live && P.has(j)) {
                 uint64_t zv[NP];
-                if constexpr (S > 0) feed.template read<T, VEC>(YOFF, j, q[j]);
+                if constexpr (S > 0) feed.template read<T, VEC>(YOFF, j, q[j], out.dst, P);
                 else load_piece<VEC>(dy + out.dst + P.col<VEC>(j), q[j]);
                 if (z) {
-                    if constexpr (S > 0) feed.template read<T, VEC>(ZOFF, j, zv);
+                    if constexpr (S > 0) feed.template read<T, VEC>(ZOFF, j, zv, out.dst, P);
                     else load_piece<VEC>(z + out.dst + P.col<VEC>(j), zv);
 #pragma unroll
                     for (int i = 0; i < NP; ++i) {
@@ -255,15 +270,15 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1)
                     r[j][i] = f2_fma(f2_mul(q[j][i], wv[j][i]), rstd2, f2_mul(n, mdn));
                     if (KIND == GLA_NORM_LAYER) r[j][i] = f2_add(r[j][i], md);
                 }
-                if (dz) store_piece<VEC>(dz + out.dst + P.col<VEC>(j), d[j]);
-                store_piece<VEC>(d_o + out.src + P.col<VEC>(j), r[j]);
+                if (dz) put_piece<VEC, ODD>(dz + out.dst, P, j, d[j]);
+                put_piece<VEC, ODD>(d_o + out.src, P, j, r[j]);
             }
         feed.next();
         walk.go(out);
     }
     grid_dep_launch();
     if (pdw)
-        write_partial<VEC, NV>(aw, reinterpret_cast<float*>(smem), grp, P, pdw + ((size_t)blockIdx.x * H + h) * D);
+        write_partial<VEC, NV, ODD>(aw, reinterpret_cast<float*>(smem), grp, P, pdw + ((size_t)blockIdx.x * H + h) * D);
 }
 
 template <typename F>
@@ -321,7 +336,7 @@ gla_status gla_headnorm_fwd(const gla_norm_problem* p, const void* o, const void
                 return by_act(p->act, [&](auto act) {
                     using Sh = decltype(sh);
                     auto kern = k_headnorm_fwd<T, Sh::vec, Sh::nv, Sh::stages, decltype(kind)::value,
-                                               decltype(act)::value, Sh::maxt>;
+                                               decltype(act)::value, Sh::maxt, Sh::odd>;
                     const size_t smem = block_smem(rp, Sh::stages, thread_bytes);
                     static std::atomic<bool> seen[kMaxDevices];
                 static Occupancy known;
@@ -365,7 +380,7 @@ gla_status gla_headnorm_bwd(const gla_norm_problem* p, const void* o, const void
                     return by_act(p->act, [&](auto act) {
                         using Sh = decltype(sh);
                         auto kern = k_headnorm_bwd<T, Sh::vec, Sh::nv, Sh::stages, decltype(kind)::value,
-                                                   decltype(act)::value, Sh::maxt>;
+                                                   decltype(act)::value, Sh::maxt, Sh::odd>;
                         const size_t smem = block_smem(rp, Sh::stages, thread_bytes);
                         static std::atomic<bool> seen[kMaxDevices];
                 static Occupancy known;

@@ -121,15 +121,45 @@ __device__ __forceinline__ void store_piece(__nv_bfloat16* p, const uint64_t (&v
     }
 }
 
-// Where a thread's pieces of a row are.
+// Where a thread's pieces of a row are. The last piece of an odd row has one column of its pair.
 struct Place {
-    int at, G, nvec;
+    int at, G, nvec, D;
     __device__ __forceinline__ bool has(int j) const { return at + j * G < nvec; }
     template <int VEC>
     __device__ __forceinline__ int col(int j) const { return (at + j * G) * VEC; }
+    __device__ __forceinline__ bool half(int j) const { return 2 * (at + j * G) + 1 == D; }
 };
 
+// Pairs of an odd row: no alignment beyond the element's, and the second column may be missing.
+__device__ __forceinline__ void store_pair(float* p, uint64_t v, bool half) {
+    float a, b;
+    f2_split(v, a, b);
+    p[0] = a;
+    if (!half) p[1] = b;
+}
+__device__ __forceinline__ void store_pair(__nv_bfloat16* p, uint64_t v, bool half) {
+    const uint32_t w = to_bf16x2(v);
+    if (!half && (reinterpret_cast<uintptr_t>(p) & 2) == 0) {
+        *reinterpret_cast<uint32_t*>(p) = w;
+        return;
+    }
+    const __nv_bfloat162 h = *reinterpret_cast<const __nv_bfloat162*>(&w);
+    p[0] = h.x;
+    if (!half) p[1] = h.y;
+}
+// Piece j of the row at `row` (element 0 of it).
+template <int VEC, bool ODD, typename T>
+__device__ __forceinline__ void put_piece(T* row, const Place& P, int j, const uint64_t (&v)[kPairs<VEC>]) {
+    if constexpr (ODD) store_pair(row + P.col<VEC>(j), v[0], P.half(j));
+    else store_piece<VEC>(row + P.col<VEC>(j), v);
+}
+
 // ------------------------------------------------------------------ the ring
+// Elements of a row that a thread of an odd row's group holds, and the room of such a row in shared memory, in
+// elements: it starts up to 14 bytes into its first 16-byte unit, and its last pair's word may be read beyond it.
+constexpr int kRowElems = 16;
+__host__ __device__ constexpr int odd_room(int G) { return kRowElems * G + 16; }
+
 // S stages of shared memory that belong to the thread alone. Piece j of an input lies in units of up to 16 bytes,
 // blockDim units of that size apart from the next piece, so that a warp's accesses are contiguous.
 // Stages are written by cp.async, one commit group per row; wait() leaves the groups of the S - 1 rows that
@@ -166,7 +196,8 @@ struct Feed {
         }
     }
     template <typename T, int VEC>
-    __device__ __forceinline__ void read(int thread_off, int j, uint64_t (&v)[kPairs<VEC>]) const {
+    __device__ __forceinline__ void read(int thread_off, int j, uint64_t (&v)[kPairs<VEC>], size_t e0,
+                                         const Place& P) const {
         constexpr int B = VEC * (int)sizeof(T);
         const uint8_t* d = at<T, VEC>(s, thread_off, j);
         if constexpr (B == 32) {   // eight fp32: two units
@@ -186,7 +217,71 @@ struct Feed {
     __device__ __forceinline__ void next() { s = s + 1 == S ? 0 : s + 1; }
 };
 
-// Without a ring (odd rows of bf16): whether the next row's pieces wait in registers instead.
+// The ring for odd rows with bf16 in them, where no copy of 4 bytes or more fits a thread's own columns: the group
+// copies the 16-byte units that the row touches, wherever in them it starts, and reads each other's, so a
+// row costs a barrier of the group's threads (wait()). Pieces are pairs; a pair that straddles two words is
+// joined from both. 16384 x 1001 in bf16, backward: 100 us; with loads of single elements 233.
+template <int S>
+struct RowFeed {
+    uint8_t* mine;      // the group's first stage
+    int stage_bytes, pad, G, s;   // pad: room of a row, in elements
+
+    __device__ __forceinline__ RowFeed(uint8_t* ring, int thread_bytes, int G_)
+        : pad(odd_room(G_)), G(G_), s(0) {
+        const int row = thread_bytes / kRowElems * pad;
+        stage_bytes = row * ((int)blockDim.x / G);
+        mine = ring + (int)threadIdx.x / G * row;
+    }
+    template <typename T, int VEC, int NV>
+    static constexpr int bytes() { return VEC * (int)sizeof(T) * NV; }
+
+    // This thread's share of the row that starts at element e0 of an input of n elements in all.
+    template <typename T>
+    __device__ __forceinline__ void copy_row(int stage, int thread_off, const T* src, size_t e0, size_t n,
+                                             const Place& P) const {
+        constexpr size_t B = sizeof(T);
+        const size_t from = e0 * B & ~(size_t)15, to = (e0 + P.D) * B, all = n * B;
+        const uint32_t d = smem_u32(mine + stage * stage_bytes + thread_off / kRowElems * pad);
+        for (int c = 16 * P.at; from + c < to; c += 16 * G) {
+            const int m = all - (from + c) < 16 ? (int)(all - (from + c)) : 16;   // the rest is filled with zeros
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d + c),
+                         "l"(reinterpret_cast<const uint8_t*>(src) + from + c), "r"(m)
+                         : "memory");
+        }
+    }
+    template <typename T, int VEC>
+    __device__ __forceinline__ void read(int thread_off, int j, uint64_t (&v)[kPairs<VEC>], size_t e0,
+                                         const Place& P) const {
+        const int at = ((int)(e0 * sizeof(T)) & 15) + P.col<VEC>(j) * (int)sizeof(T);
+        const uint8_t* d = mine + s * stage_bytes + thread_off / kRowElems * pad;
+        if constexpr (sizeof(T) == 4) {
+            const float* f = reinterpret_cast<const float*>(d + at);
+            const float b = f[1];
+            v[0] = f2(f[0], P.half(j) ? 0.f : b);
+        } else {
+            const uint32_t* w = reinterpret_cast<const uint32_t*>(d + (at & ~3));
+            uint32_t u = w[0];
+            if (at & 2) u = __funnelshift_r(u, w[1], 16);
+            v[0] = f2(__uint_as_float(u << 16), P.half(j) ? 0.f : __uint_as_float(u & 0xffff0000u));
+        }
+    }
+    __device__ __forceinline__ void commit() const { asm volatile("cp.async.commit_group;" ::: "memory"); }
+    // Waits for the row of stage s, and until the group has read the stage before it.
+    __device__ __forceinline__ void wait() const {
+        asm volatile("cp.async.wait_group %0;" ::"n"(S > 2 ? S - 2 : 0) : "memory");
+        if (G > 32) __syncthreads();
+        else __syncwarp();
+    }
+    __device__ __forceinline__ int ahead() const { return s == 0 ? S - 1 : s - 1; }
+    __device__ __forceinline__ void next() { s = s + 1 == S ? 0 : s + 1; }
+};
+template <int S, bool ODD>
+__device__ __forceinline__ auto make_feed(uint8_t* ring, int thread_bytes, int G) {
+    if constexpr (ODD) return RowFeed<S>(ring, thread_bytes, G);
+    else return Feed<S>{ring + 16 * threadIdx.x, thread_bytes * (int)blockDim.x, 0};
+}
+
+// Without a ring (long rows of pairs, with fp32 among them): whether the next row's pieces wait in registers instead.
 template <int S, int NV>
 constexpr bool kHold = S == 0 && NV <= 4;
 
@@ -253,7 +348,7 @@ struct RowSum {
 };
 
 // r -= mean(r) for the layer norm (elements beyond the row stay 0).
-template <int KIND, int VEC, int NV>
+template <int KIND, int VEC, int NV, bool ODD>
 __device__ __forceinline__ void center(RowSum& sum, uint64_t (&r)[NV][kPairs<VEC>], const Place& P, float inv_d) {
     if (KIND != GLA_NORM_LAYER) return;
     uint64_t t = 0;
@@ -269,7 +364,7 @@ __device__ __forceinline__ void center(RowSum& sum, uint64_t (&r)[NV][kPairs<VEC
     for (int j = 0; j < NV; ++j)
         if (P.has(j))
 #pragma unroll
-            for (int i = 0; i < kPairs<VEC>; ++i) r[j][i] = f2_add(r[j][i], m2);
+            for (int i = 0; i < kPairs<VEC>; ++i) r[j][i] = f2_add(r[j][i], ODD && P.half(j) ? f2(mu, 0.f) : m2);
 }
 
 template <int VEC, int NV>
@@ -283,13 +378,17 @@ __device__ __forceinline__ float square_sum(const uint64_t (&r)[NV][kPairs<VEC>]
 }
 
 // This thread's columns of a weight vector times c (null: c).
-template <int VEC, int NV>
+template <int VEC, int NV, bool ODD>
 __device__ __forceinline__ void load_columns(uint64_t (&v)[NV][kPairs<VEC>], const float* p, const Place& P, float c) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
 #pragma unroll
         for (int i = 0; i < kPairs<VEC>; ++i) v[j][i] = f2_all(1.f);
-        if (p && P.has(j)) load_piece<VEC>(p + P.col<VEC>(j), v[j]);
+        if (p && P.has(j)) {
+            const float* c0 = p + P.col<VEC>(j);
+            if constexpr (ODD) v[j][0] = f2(c0[0], P.half(j) ? 1.f : c0[1]);
+            else load_piece<VEC>(c0, v[j]);
+        }
 #pragma unroll
         for (int i = 0; i < kPairs<VEC>; ++i) v[j][i] = f2_mul(v[j][i], f2_all(c));
     }
@@ -297,14 +396,14 @@ __device__ __forceinline__ void load_columns(uint64_t (&v)[NV][kPairs<VEC>], con
 
 // Sums a column accumulator over the row groups of a block and writes the block's partial row.
 // smem: blockDim * NV * VEC floats where the block has several rows.
-template <int VEC, int NV>
+template <int VEC, int NV, bool ODD>
 __device__ __forceinline__ void write_partial(const uint64_t (&acc)[NV][kPairs<VEC>], float* smem, int grp,
                                               const Place& P, float* out) {
-    const int D = P.nvec * VEC, ngrp = P.G >= 32 && P.G == (int)blockDim.x ? 1 : blockDim.x / P.G;
+    const int D = P.D, ngrp = P.G >= 32 && P.G == (int)blockDim.x ? 1 : blockDim.x / P.G;
     if (ngrp == 1) {
 #pragma unroll
         for (int j = 0; j < NV; ++j)
-            if (P.has(j)) store_piece<VEC>(out + P.col<VEC>(j), acc[j]);
+            if (P.has(j)) put_piece<VEC, ODD>(out, P, j, acc[j]);
         return;
     }
     __syncthreads();
@@ -316,7 +415,7 @@ __device__ __forceinline__ void write_partial(const uint64_t (&acc)[NV][kPairs<V
                 float a, b;
                 f2_split(acc[j][i], a, b);
                 smem[grp * D + P.col<VEC>(j) + 2 * i] = a;
-                if (VEC > 1) smem[grp * D + P.col<VEC>(j) + 2 * i + 1] = b;
+                if (VEC > 1 && !(ODD && P.half(j))) smem[grp * D + P.col<VEC>(j) + 2 * i + 1] = b;
             }
     __syncthreads();
     for (int c = threadIdx.x; c < D; c += blockDim.x) {
@@ -368,18 +467,21 @@ inline cudaError_t colsum(const float* part0, float* out0, const float* part1, f
 // Threads and pieces of a row. A piece is 16 bytes of the widest type in the row (8 bf16, or 4 where
 // fp32 stands beside them: with 8 the fp32 accesses of a warp would leave every other 16 bytes out,
 // 305 instead of 212 us for the backward of 16384 x 4096 with an fp32 residual), 4 elements where D is no
-// multiple of 8, then 2, then 1. A thread holds 16 elements, so that the row sums' exchange and the
+// multiple of 8, then 2, then 1; pairs in an odd row with bf16 (RowFeed), up to 512 threads. A thread holds 16 elements, so that the row sums' exchange and the
 // addresses of a row are spread over many; with narrower pieces 4 of them while 512 threads do. A row has a
 // power of two of lanes up to a warp, whole warps beyond.
 struct RowPlan {
     int vec, nv, G, threads;
-    bool ring;   // pieces of 4 bytes or more in every operand, at most 512 threads
+    bool ring;   // pieces of 4 bytes or more in every operand, or rows of a RowFeed; at most 512 threads
+    bool odd;    // of a RowFeed
 };
 inline RowPlan row_plan(int D, bool all_bf16, bool all_f32) {
     RowPlan p;
     p.vec = all_bf16 && D % 8 == 0 ? 8 : D % 4 == 0 ? 4 : D % 2 == 0 ? 2 : 1;
-    const int nvec = D / p.vec;
-    p.nv = p.vec < 4 && nvec <= 2048 ? 4 : 16 / p.vec;
+    p.odd = D % 2 == 1 && !all_f32 && D <= 512 * kRowElems;
+    if (p.odd) p.vec = 2;
+    const int nvec = cdiv(D, p.vec);
+    p.nv = p.odd ? kRowElems / 2 : p.vec < 4 && nvec <= 2048 ? 4 : 16 / p.vec;
     const int need = cdiv(nvec, p.nv);
     if (need > 32) {
         p.G = cdiv(need, 32) * 32;
@@ -388,7 +490,7 @@ inline RowPlan row_plan(int D, bool all_bf16, bool all_f32) {
         for (p.G = 1; p.G < need;) p.G *= 2;
         p.threads = 256;
     }
-    p.ring = p.threads <= 512 && (p.vec > 1 || all_f32) && !(p.vec < 4 && p.nv > 4);
+    p.ring = p.odd || p.threads <= 512 && (p.vec > 1 || all_f32) && !(p.vec < 4 && p.nv > 4);
     return p;
 }
 // Shared memory in front of the ring: the row sums' buffer; it and the ring are free again when the column
@@ -396,14 +498,17 @@ inline RowPlan row_plan(int D, bool all_bf16, bool all_f32) {
 constexpr int kHead = 1024;
 constexpr int kSmSmem = 220 * 1024;    // of an SM, for its blocks
 // Stages of the ring: 3 where two blocks of them fit an SM, else 2 where one does, else none.
+inline int stage_bytes(const RowPlan& p, int thread_bytes) {
+    return p.odd ? thread_bytes / kRowElems * odd_room(p.G) * (p.threads / p.G) : thread_bytes * p.threads;
+}
 inline int ring_stages(const RowPlan& p, int thread_bytes) {
-    const int row = thread_bytes * p.threads;
+    const int row = stage_bytes(p, thread_bytes);
     if (!p.ring) return 0;
     if (2 * (3 * row + kHead + 1024) <= kSmSmem) return 3;
     return 2 * row + kHead + 1024 <= kSmSmem ? 2 : 0;
 }
 inline size_t block_smem(const RowPlan& p, int stages, int thread_bytes) {
-    const size_t ring = kHead + (size_t)stages * thread_bytes * p.threads;
+    const size_t ring = kHead + (size_t)stages * stage_bytes(p, thread_bytes);
     const size_t cols = p.threads == p.G ? 0 : (size_t)4 * p.threads * p.nv * p.vec;
     return ring > cols ? ring : cols;
 }
@@ -418,15 +523,15 @@ inline int row_blocks(const RowPlan& p, long long rows, int heads) {
     if (most < 1) most = 1;
     return (int)(need < most ? need : most);
 }
-// Blocks of `kern` that an SM holds, asked of the runtime once per kernel, device and block size (`known`;
-// a kernel's shared memory follows from its block size).
-using Occupancy = std::atomic<int>[kMaxDevices][33];
+// Blocks of `kern` that an SM holds, asked of the runtime once per kernel, device, threads and group (`known`;
+// a kernel's shared memory follows from these; groups below a warp are 1, 2, 4, 8, 16).
+using Occupancy = std::atomic<int>[kMaxDevices][33 + 32];
 template <typename K>
 int fit_blocks(K kern, const RowPlan& p, size_t smem, int blocks, int heads, Occupancy& known) {
     if ((long long)blocks * heads <= tc::num_sms()) return blocks;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return blocks;
-    std::atomic<int>& slot = known[dev][p.threads / 32];
+    std::atomic<int>& slot = known[dev][p.threads / 32 + (p.G < 32 ? 33 : 0) + (p.G < 32 ? p.G : 0)];
     int per_sm = slot.load(std::memory_order_relaxed);
     if (per_sm == 0) {
         if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, p.threads, smem) != cudaSuccess ||
@@ -441,24 +546,26 @@ int fit_blocks(K kern, const RowPlan& p, size_t smem, int blocks, int heads, Occ
 }
 
 // Picks the kernel's shape: VEC, NV, ring stages, largest block.
-template <int V, int N, int S, int M> struct Shape {
+template <int V, int N, int S, int M, bool O = false> struct Shape {
     static constexpr int vec = V, nv = N, stages = S, maxt = M;
+    static constexpr bool odd = O;
 };
 // BF16, F32: every operand of the row has that type, so pieces of 8, and a ring of single elements, exist too.
 // Blocks of up to 256 threads (D <= 4096 with pieces of 4 or 8) have kernels of their own, which need not fit their
 // registers into a larger block's share. Without a ring up to 1024 threads: with 16 elements each they
 // spill; only rows beyond 8192 elements, or too long for two stages.
-template <int V, int N, int S, typename F>
+template <int V, int N, int S, bool O = false, typename F>
 cudaError_t by_block(const RowPlan& p, F&& f) {
-    return p.threads <= 256 ? f(Shape<V, N, S, 256>{}) : f(Shape<V, N, S, 512>{});
+    return p.threads <= 256 ? f(Shape<V, N, S, 256, O>{}) : f(Shape<V, N, S, 512, O>{});
 }
 template <bool BF16, bool F32, typename F>
 cudaError_t by_shape(const RowPlan& p, int stages, F&& f) {
+    if constexpr (!F32)
+        if (p.odd) return stages == 3 ? by_block<2, 8, 3, true>(p, f) : f(Shape<2, 8, 2, 512, true>{});
     if (p.vec == 1) {
-        if (p.nv == 16) return f(Shape<1, 16, 0, 1024>{});
         if constexpr (F32)
-            if (stages == 3) return by_block<1, 4, 3>(p, f);
-        return by_block<1, 4, 0>(p, f);
+            if (p.nv == 4) return by_block<1, 4, 3>(p, f);   // three stages of 512 threads fit twice
+        return f(Shape<1, 16, 0, 1024>{});
     }
     if (p.vec == 2) {
         if (p.nv == 8) return f(Shape<2, 8, 0, 1024>{});

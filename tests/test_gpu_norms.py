@@ -67,7 +67,8 @@ def grad_bound(r, d, kind):
 
 ROWS = [(1, 1), (3, 7), (5, 8), (1, 33), (64, 64), (70, 100), (9, 257), (33, 256), (17, 512), (700, 520), (2, 1000),
         (5, 2048), (300, 2052), (3, 4096), (4, 4104), (2, 8192), (3, 8200), (2, 9999), (2, 16384),
-        (400, 66), (2000, 78), (900, 330), (700, 333), (5, 2050), (3, 4098), (3, 4100), (2, 2049), (900, 1185)]
+        (400, 66), (2000, 78), (900, 330), (700, 333), (5, 2050), (3, 4098), (3, 4100), (2, 2049), (900, 1185),
+        (301, 17), (70, 101), (2000, 9), (3, 4097), (300, 3001), (5, 8191), (2, 8193)]
 
 
 def addnorm_inputs(N, D, io, res, seed):
@@ -136,7 +137,8 @@ def test_addnorm_optional_arguments(rscale, w, resid, dr):
 
 HEADS = [(1, 1, 1, 1), (2, 3, 5, 7), (1, 2, 3, 8), (2, 2, 33, 64), (3, 5, 21, 100), (1, 4, 130, 128), (2, 3, 40, 256),
          (1, 17, 9, 36), (64, 4, 1, 64), (1, 2, 300, 24), (1, 2, 4, 512), (2, 1, 3, 1028), (1, 2, 2, 4096), (1, 1, 2, 9001),
-         (3, 5, 700, 50), (2, 3, 200, 258), (3, 2, 500, 75), (1, 1, 2, 4102)]
+         (3, 5, 700, 50), (2, 3, 200, 258), (3, 2, 500, 75), (1, 1, 2, 4102), (3, 5, 301, 9), (2, 3, 71, 101),
+         (2, 3, 17, 129), (1, 3, 41, 1001), (1, 2, 5, 4095), (1, 2, 3, 8191)]
 
 
 def headnorm_inputs(B, H, L, D, io, per_head, seed):
