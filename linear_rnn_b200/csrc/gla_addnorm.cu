@@ -287,8 +287,8 @@ cudaError_t by_dtypes(gla_dtype io, gla_dtype res, F&& f) {
     return res == GLA_F32 ? f(__nv_bfloat16{}, float{}) : f(__nv_bfloat16{}, __nv_bfloat16{});
 }
 
-RowPlan plan(const gla_norm_problem* p) {
-    return row_plan(p->D, p->io == GLA_BF16 && p->res == GLA_BF16, p->io == GLA_F32);
+RowPlan plan(const gla_norm_problem* p, bool bwd) {
+    return row_plan(p->D, p->io == GLA_BF16 && p->res == GLA_BF16, p->io == GLA_F32, bwd);
 }
 
 gla_status check(const gla_norm_problem* p) {
@@ -309,7 +309,7 @@ extern "C" {
 
 size_t gla_addnorm_workspace_bytes(const gla_norm_problem* p) {
     if (check(p) != GLA_OK) return 0;
-    const int P = row_blocks(plan(p), (long long)p->B * p->L, 1);
+    const int P = row_blocks(plan(p, true), (long long)p->B * p->L, 1);
     return P > 1 ? 256 + 2 * align_up((size_t)P * p->D * 4, 256) : 256;
 }
 
@@ -323,13 +323,13 @@ gla_status gla_addnorm_fwd(const gla_norm_problem* p, const void* x, const void*
     if (rows == 0) return GLA_OK;
     if (!x || !y) return GLA_ERR_INVALID_ARG;
     cudaStream_t st = (cudaStream_t)stream;
-    const RowPlan rp = plan(p);
+    const RowPlan rp = plan(p, false);
     const cudaError_t e = by_dtypes(p->io, p->res, [&](auto tv, auto rv) {
         using T = decltype(tv);
         using R = decltype(rv);
         const int thread_bytes = rp.nv * rp.vec * (int)(sizeof(T) + sizeof(R));
         const int stages = ring_stages(rp, thread_bytes);
-        return by_shape<sizeof(T) + sizeof(R) == 4, sizeof(T) == 4>(rp, stages, [&](auto sh) {
+        return by_shape<sizeof(T) + sizeof(R) == 4, sizeof(T) == 4, false>(rp, stages, [&](auto sh) {
             return by_kind(p->kind, [&](auto kind) {
                 using Sh = decltype(sh);
                 auto kern = k_addnorm_fwd<T, R, Sh::vec, Sh::nv, Sh::stages, decltype(kind)::value, Sh::maxt, Sh::odd>;
@@ -357,7 +357,7 @@ gla_status gla_addnorm_bwd(const gla_norm_problem* p, const void* x, const void*
     if (s != GLA_OK) return s;
     const void* const ptrs[] = {x, r, rscale, w, dy, dr, dres, dx, dw, drscale, ws};
     const int rows = p->B * p->L;
-    const RowPlan rp = plan(p);
+    const RowPlan rp = plan(p, true);
     int P = row_blocks(rp, rows, 1);
     const bool direct = P == 1;   // a single block's sums are the result
     if (!all_aligned(ptrs) || (!ws && P > 1)) return GLA_ERR_INVALID_ARG;
@@ -376,7 +376,7 @@ gla_status gla_addnorm_bwd(const gla_norm_problem* p, const void* x, const void*
             using R = decltype(rv);
             const int thread_bytes = 2 * rp.nv * rp.vec * (int)(sizeof(T) + sizeof(R));
             const int stages = ring_stages(rp, thread_bytes);
-            return by_shape<sizeof(T) + sizeof(R) == 4, sizeof(T) == 4>(rp, stages, [&](auto sh) {
+            return by_shape<sizeof(T) + sizeof(R) == 4, sizeof(T) == 4, true>(rp, stages, [&](auto sh) {
                 return by_kind(p->kind, [&](auto kind) {
                     using Sh = decltype(sh);
                     auto kern = k_addnorm_bwd<T, R, Sh::vec, Sh::nv, Sh::stages, decltype(kind)::value, Sh::maxt, Sh::odd>;

@@ -467,21 +467,26 @@ inline cudaError_t colsum(const float* part0, float* out0, const float* part1, f
 // Threads and pieces of a row. A piece is 16 bytes of the widest type in the row (8 bf16, or 4 where
 // fp32 stands beside them: with 8 the fp32 accesses of a warp would leave every other 16 bytes out,
 // 305 instead of 212 us for the backward of 16384 x 4096 with an fp32 residual), 4 elements where D is no
-// multiple of 8, then 2, then 1; pairs in an odd row with bf16 (RowFeed), up to 512 threads. A thread holds 16 elements, so that the row sums' exchange and the
-// addresses of a row are spread over many; with narrower pieces 4 of them while 512 threads do. A row has a
-// power of two of lanes up to a warp, whole warps beyond.
+// multiple of 8, then 2, then 1; pairs in an odd row with bf16 (RowFeed), up to 512 threads. A thread
+// holds 16 elements, so that the row sums' exchange and the addresses of a row are spread over many; with narrower
+// pieces 4 of them while 512 threads do. A row has a power of two of lanes up to a warp, whole warps beyond.
 struct RowPlan {
     int vec, nv, G, threads;
-    bool ring;   // pieces of 4 bytes or more in every operand, or rows of a RowFeed; at most 512 threads
+    bool ring;   // pieces of 4 bytes or more in every operand, or rows of a RowFeed; at most 512 threads (kWide)
     bool odd;    // of a RowFeed
 };
-inline RowPlan row_plan(int D, bool all_bf16, bool all_f32) {
+// wide_rows: 8 elements a thread for 4096 < D <= 6144, where 16 would leave an SM one block of 9 to 12 warps, their
+// registers too many for two. addnorm backward, 16384 x 5120 in bf16: 240 us, 287 with 16 elements; the
+// forward, of fewer registers, loses (16384 x 6144 with an fp32 residual: 219, and 196 with 16).
+constexpr int kWide = 768;
+inline RowPlan row_plan(int D, bool all_bf16, bool all_f32, bool wide_rows = false) {
     RowPlan p;
     p.vec = all_bf16 && D % 8 == 0 ? 8 : D % 4 == 0 ? 4 : D % 2 == 0 ? 2 : 1;
     p.odd = D % 2 == 1 && !all_f32 && D <= 512 * kRowElems;
     if (p.odd) p.vec = 2;
     const int nvec = cdiv(D, p.vec);
-    p.nv = p.odd ? kRowElems / 2 : p.vec < 4 && nvec <= 2048 ? 4 : 16 / p.vec;
+    const bool wide = wide_rows && p.vec >= 4 && D > 4096 && D <= 8 * kWide;
+    p.nv = p.odd ? kRowElems / 2 : wide ? 8 / p.vec : p.vec < 4 && nvec <= 2048 ? 4 : 16 / p.vec;
     const int need = cdiv(nvec, p.nv);
     if (need > 32) {
         p.G = cdiv(need, 32) * 32;
@@ -490,7 +495,7 @@ inline RowPlan row_plan(int D, bool all_bf16, bool all_f32) {
         for (p.G = 1; p.G < need;) p.G *= 2;
         p.threads = 256;
     }
-    p.ring = p.odd || p.threads <= 512 && (p.vec > 1 || all_f32) && !(p.vec < 4 && p.nv > 4);
+    p.ring = p.odd || p.threads <= (wide ? kWide : 512) && (p.vec > 1 || all_f32) && !(p.vec < 4 && p.nv > 4);
     return p;
 }
 // Shared memory in front of the ring: the row sums' buffer; it and the ring are free again when the column
@@ -558,7 +563,7 @@ template <int V, int N, int S, bool O = false, typename F>
 cudaError_t by_block(const RowPlan& p, F&& f) {
     return p.threads <= 256 ? f(Shape<V, N, S, 256, O>{}) : f(Shape<V, N, S, 512, O>{});
 }
-template <bool BF16, bool F32, typename F>
+template <bool BF16, bool F32, bool WIDE, typename F>
 cudaError_t by_shape(const RowPlan& p, int stages, F&& f) {
     if constexpr (!F32)
         if (p.odd) return stages == 3 ? by_block<2, 8, 3, true>(p, f) : f(Shape<2, 8, 2, 512, true>{});
@@ -571,6 +576,14 @@ cudaError_t by_shape(const RowPlan& p, int stages, F&& f) {
         if (p.nv == 8) return f(Shape<2, 8, 0, 1024>{});
         return stages == 3 ? by_block<2, 4, 3>(p, f) : f(Shape<2, 4, 0, 512>{});
     }
+    if constexpr (WIDE)
+        if (p.vec * p.nv == 8) {
+            if constexpr (BF16) {
+                if (p.vec == 8) return stages == 3 ? f(Shape<8, 1, 3, kWide>{}) : f(Shape<8, 1, 2, kWide>{});
+                if (stages == 3) return f(Shape<4, 2, 3, kWide>{});
+            }
+            return f(Shape<4, 2, 2, kWide>{});
+        }
     if constexpr (BF16)
         if (p.vec == 8)
             return stages == 3   ? by_block<8, 2, 3>(p, f)
