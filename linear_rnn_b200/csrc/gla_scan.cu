@@ -841,8 +841,9 @@ gla_status check(const gla_problem* p) {
     if (p->io != GLA_F32 && p->io != GLA_BF16) return GLA_ERR_INVALID_ARG;
     if (p->gate != GLA_GATE_PER_KEY) return GLA_ERR_INVALID_ARG;
     if (p->Dk > 65536 || p->L > 1 << 30) return GLA_ERR_UNSUPPORTED;
-    // at most 2^27 clusters of 8
-    if ((long long)p->B * p->H * cdiv(p->Dk, 32) > 1 << 27) return GLA_ERR_UNSUPPORTED;
+    // at most 2^27 chains; B * H first, as the product of all three may pass 64 bits
+    const long long bh = (long long)p->B * p->H;
+    if (bh > 1 << 27 || bh * cdiv(p->Dk, CH) > 1 << 27) return GLA_ERR_UNSUPPORTED;
     return GLA_OK;
 }
 bool input_ok(int input) { return input >= GLA_SCAN_PLAIN && input <= GLA_SCAN_NORM; }

@@ -22,7 +22,8 @@ def prob(**kw):
 
 BAD_SCAN = [(dict(B=-1), INVALID), (dict(L=-1), INVALID), (dict(D=0), INVALID), (dict(Dk=64), INVALID),
             (dict(io=2), INVALID), (dict(gate=_lib.GLA_GATE_NONE), INVALID), (dict(gate=_lib.GLA_GATE_PER_HEAD), INVALID),
-            (dict(D=65537), UNSUPPORTED), (dict(B=1 << 20, H=1 << 20), UNSUPPORTED)]
+            (dict(D=65537), UNSUPPORTED), (dict(B=1 << 20, H=1 << 20), UNSUPPORTED),
+            (dict(B=(1 << 31) - 1, H=(1 << 31) - 1, D=65536), UNSUPPORTED)]
 
 
 def scan_fwd(p, input=0, **kw):
