@@ -351,10 +351,11 @@ def _launch(where, fn, dev, args):
 
 
 def _from_host(fn, tensors, kw):
-    """A call on host tensors: copies to the current device, the call, copies back."""
+    """A call on host tensors: copies to the current device, the call, copies back. The caller's buffers are not
+    copied: they are written, and must be on the device."""
     device = torch.device("cuda", torch.cuda.current_device())
     moved = [t if t is None or t.is_cuda else t.contiguous().to(device, non_blocking=True) for t in tensors]
-    kw = {k: v.to(device) if isinstance(v, torch.Tensor) and not v.is_cuda else v for k, v in kw.items()}
+    kw = {k: v.to(device) if k == "rscale" and v is not None else v for k, v in kw.items()}
     out = fn(*moved, **kw)
     if isinstance(out, dict):
         return dict(zip(out, _to_host(list(out.values()))))
@@ -376,7 +377,8 @@ _descriptors = {}
 
 
 def _descriptor(key, make):
-    """The C descriptor of a problem, made once per sizes and types: (struct, reference to it)."""
+    """The C descriptor of a problem, made once per sizes and types: (struct, reference to it). The key holds
+    plain numbers only: a tensor in it would be found by its identity, whatever its value had become."""
     d = _descriptors.get(key)
     if d is None:
         if len(_descriptors) >= 1024:
@@ -511,7 +513,7 @@ def gla_addnorm_fwd(x, res=None, w=None, *, rscale=None, alpha: float = 1.0, kin
     if not x.is_cuda:
         return _from_host(gla_addnorm_fwd, (x, res, w),
                           dict(rscale=rscale, alpha=alpha, kind=kind, eps=eps, res_dtype=res_dtype))
-    shape, dtype, dev = x.shape, x.dtype, x.get_device()
+    shape, dtype, dev, alpha, eps = x.shape, x.dtype, x.get_device(), float(alpha), float(eps)
     if res is not None:
         if res_dtype not in (None, res.dtype):
             raise ValueError("res_dtype is res's dtype when res is given")
@@ -552,10 +554,11 @@ def gla_addnorm_bwd(x, r, w, dy, dr=None, *, rscale=None, alpha: float = 1.0, ki
     rscale). x is only read for drscale and may be None without rscale; dr [..., D] is the
     gradient that reaches r from later blocks, or None."""
     if not dy.is_cuda:
-        return _from_host(gla_addnorm_bwd, (x, r, w, dy, dr),
+        return _from_host(gla_addnorm_bwd, (x, _need("r", r), w, dy, dr),
                           dict(rscale=rscale, alpha=alpha, kind=kind, eps=eps, output_dx=output_dx,
                                workspace=workspace))
-    shape, dtype, dev, res_dtype = dy.shape, dy.dtype, dy.get_device(), r.dtype
+    shape, dtype, dev, res_dtype = dy.shape, dy.dtype, dy.get_device(), _need("r", r).dtype
+    alpha, eps = float(alpha), float(eps)
     _, ref = _descriptor((shape, dtype, res_dtype, kind, eps, alpha),
                          lambda: _addnorm_problem(dy, res_dtype, kind, eps, alpha))
     cols = shape[-1:]
@@ -596,7 +599,7 @@ def gla_headnorm_fwd(o, z=None, w=None, *, act: str = "silu", kind: str = "rms",
     Host tensors are copied to the current device and the result back."""
     if not o.is_cuda:
         return _from_host(gla_headnorm_fwd, (o, z, w), dict(act=act, kind=kind, eps=eps))
-    shape, dtype, dev = o.shape, o.dtype, o.get_device()
+    shape, dtype, dev, eps = o.shape, o.dtype, o.get_device(), float(eps)
     heads = w is not None and w.dim() == 2
     _, ref = _descriptor((shape, dtype, heads, act, kind, eps), lambda: _headnorm_problem(o, w, act, kind, eps))
     B, H, L, D = shape
@@ -616,7 +619,7 @@ def gla_headnorm_bwd(o, z, w, dy, *, act: str = "silu", kind: str = "rms", eps: 
     if not o.is_cuda:
         return _from_host(gla_headnorm_bwd, (o, z, w, _need("dy", dy)),
                           dict(act=act, kind=kind, eps=eps, workspace=workspace))
-    shape, dtype, dev = o.shape, o.dtype, o.get_device()
+    shape, dtype, dev, eps = o.shape, o.dtype, o.get_device(), float(eps)
     heads = w is not None and w.dim() == 2
     _, ref = _descriptor((shape, dtype, heads, act, kind, eps), lambda: _headnorm_problem(o, w, act, kind, eps))
     B, H, L, D = shape

@@ -562,3 +562,42 @@ def test_host_threads_with_their_own_streams():
     for t in threads:
         t.join()
     assert not bad
+
+
+def test_a_changed_scalar_is_seen():
+    """alpha and eps given as tensors are read at each call."""
+    from linear_rnn_b200 import ops
+    x, r0 = torch.randn(5, 64).cuda(), torch.randn(5, 64).cuda()
+    alpha, eps = torch.tensor(2.0), torch.tensor(1e-6)
+    ops.gla_addnorm_fwd(x, r0, alpha=alpha, eps=eps)
+    ops.gla_headnorm_fwd(x.view(1, 1, 5, 64), eps=eps)
+    alpha.fill_(3.0)
+    eps.fill_(0.5)
+    r, y = ops.gla_addnorm_fwd(x, r0, alpha=alpha, eps=eps)
+    want_r, want_y = ops.gla_addnorm_fwd(x, r0, alpha=3.0, eps=0.5)
+    assert torch.equal(r, want_r) and torch.equal(y, want_y)
+    got = ops.gla_addnorm_bwd(None, r, None, x, alpha=alpha, eps=eps)
+    want = ops.gla_addnorm_bwd(None, r, None, x, alpha=3.0, eps=0.5)
+    assert torch.equal(got["dres"], want["dres"]) and torch.equal(got["dx"], want["dx"])
+    o = x.view(1, 1, 5, 64)
+    assert torch.equal(ops.gla_headnorm_fwd(o, eps=eps), ops.gla_headnorm_fwd(o, eps=0.5))
+
+
+def test_buffers_on_the_host_are_refused():
+    """A host buffer next to host tensors would be written on the device only."""
+    from linear_rnn_b200 import ops
+    x, g = torch.randn(1, 1, 100, 8), -torch.rand(1, 1, 100, 8)
+    buf = torch.zeros(1 << 16, dtype=torch.uint8)
+    with pytest.raises(ValueError):
+        ops.gla_scan_fwd(x, g, saved_states=buf)
+    with pytest.raises(ValueError):
+        ops.gla_scan_bwd(x, g, None, x, saved_states=buf)
+    with pytest.raises(ValueError):
+        ops.gla_scan_bwd(x, g, None, x, workspace=buf)
+    with pytest.raises(ValueError):
+        ops.gla_addnorm_bwd(None, x, None, x, workspace=buf)
+    with pytest.raises(ValueError):
+        ops.gla_headnorm_bwd(x, None, None, x.view(1, 100, 1, 8), workspace=buf)
+    o, hT = ops.gla_scan_fwd(x, g, saved_states=buf.cuda())
+    want_o, want_hT = ops.gla_scan_fwd(x, g)
+    assert torch.equal(o, want_o) and torch.equal(hT, want_hT)
