@@ -54,18 +54,6 @@ __global__ void __launch_bounds__(MAXT, ODD || (MAXT == 256 && VEC == 8) ? (MAXT
     };
 #pragma unroll
     for (int k = 0; k + 1 < S; ++k) copy(row + k * step, k);
-    uint64_t xn[NV][NP] = {}, rn[NV][NP] = {};
-    auto hold = [&](long long to) {
-        if (kHold<S, NV> && to < rows)
-#pragma unroll
-            for (int j = 0; j < NV; ++j)
-                if (P.has(j)) {
-                    const size_t c = (size_t)to * D + P.col<VEC>(j);
-                    load_piece<VEC>(x + c, xn[j]);
-                    if (res) load_piece<VEC>(res + c, rn[j]);
-                }
-    };
-    hold(row);
     // every group of a block takes as many turns: the row sums are the block's business
     for (long long first = (long long)blockIdx.x * ngrp; first < rows; first += step, row += step) {
         const bool live = row < rows;
@@ -84,9 +72,6 @@ __global__ void __launch_bounds__(MAXT, ODD || (MAXT == 256 && VEC == 8) ? (MAXT
                 if constexpr (S > 0) {
                     feed.template read<T, VEC>(XOFF, j, xv, off, P);
                     if (res) feed.template read<R, VEC>(0, j, r[j], off, P);
-                } else if constexpr (kHold<S, NV>) {
-#pragma unroll
-                    for (int i = 0; i < NP; ++i) xv[i] = xn[j][i], r[j][i] = rn[j][i];
                 } else {
                     load_piece<VEC>(x + off + P.col<VEC>(j), xv);
                     if (res) load_piece<VEC>(res + off + P.col<VEC>(j), r[j]);
@@ -96,7 +81,6 @@ __global__ void __launch_bounds__(MAXT, ODD || (MAXT == 256 && VEC == 8) ? (MAXT
                 if (r_out) put_piece<VEC, ODD>(r_out + off, P, j, r[j]);
             }
         }
-        hold(row + step);
         center<KIND, VEC, NV, ODD>(sum, r, P, inv_d);
         float s[1] = {square_sum<VEC, NV>(r)};
         sum(s);
@@ -158,20 +142,6 @@ __global__ void __launch_bounds__(MAXT < 512 ? 448 : MAXT)   // 144 registers. 1
     };
 #pragma unroll
     for (int k = 0; k + 1 < S; ++k) copy(row + k * step, k);
-    uint64_t rn[NV][NP] = {}, dn[NV][NP] = {}, drn[NV][NP] = {}, xn[NV][NP] = {};
-    auto hold = [&](long long to) {
-        if (kHold<S, NV> && to < rows)
-#pragma unroll
-            for (int j = 0; j < NV; ++j)
-                if (P.has(j)) {
-                    const size_t c = (size_t)to * D + P.col<VEC>(j);
-                    load_piece<VEC>(r_in + c, rn[j]);
-                    load_piece<VEC>(dy + c, dn[j]);
-                    if (dr) load_piece<VEC>(dr + c, drn[j]);
-                    if (pds) load_piece<VEC>(x + c, xn[j]);
-                }
-    };
-    hold(row);
     for (long long first = (long long)blockIdx.x * ngrp; first < rows; first += step, row += step) {
         const bool live = row < rows;
         const size_t off = (size_t)row * D;
@@ -180,28 +150,20 @@ __global__ void __launch_bounds__(MAXT < 512 ? 448 : MAXT)   // 144 registers. 1
             copy(row + (S - 1) * step, feed.ahead());
         }
         uint64_t r[NV][NP], d[NV][NP];   // r - mu, then n; dy, then d = dy w
-        uint64_t drc[NV][NP], xc[NV][NP];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            if (kHold<S, NV>)
-#pragma unroll
-                for (int i = 0; i < NP; ++i) drc[j][i] = drn[j][i], xc[j][i] = xn[j][i];
 #pragma unroll
             for (int i = 0; i < NP; ++i) r[j][i] = d[j][i] = 0;
             if (live && P.has(j)) {
                 if constexpr (S > 0) {
                     feed.template read<R, VEC>(0, j, r[j], off, P);
                     feed.template read<T, VEC>(DYOFF, j, d[j], off, P);
-                } else if constexpr (kHold<S, NV>) {
-#pragma unroll
-                    for (int i = 0; i < NP; ++i) r[j][i] = rn[j][i], d[j][i] = dn[j][i];
                 } else {
                     load_piece<VEC>(r_in + off + P.col<VEC>(j), r[j]);
                     load_piece<VEC>(dy + off + P.col<VEC>(j), d[j]);
                 }
             }
         }
-        hold(row + step);
         center<KIND, VEC, NV, ODD>(sum, r, P, inv_d);
         // sums of (r - mu)^2, d (r - mu) and, for the layer norm, d
         uint64_t t0 = 0, t1 = 0, t2 = 0;
@@ -233,9 +195,6 @@ __global__ void __launch_bounds__(MAXT < 512 ? 448 : MAXT)   // 144 registers. 1
                 if (dr) {
                     if constexpr (S > 0) {
                         feed.template read<R, VEC>(DROFF, j, t, off, P);
-                    } else if constexpr (kHold<S, NV>) {
-#pragma unroll
-                        for (int i = 0; i < NP; ++i) t[i] = drc[j][i];
                     } else {
                         load_piece<VEC>(dr + off + P.col<VEC>(j), t);
                     }
@@ -252,9 +211,6 @@ __global__ void __launch_bounds__(MAXT < 512 ? 448 : MAXT)   // 144 registers. 1
                 if (pds) {
                     if constexpr (S > 0) {
                         feed.template read<T, VEC>(XOFF, j, xv, off, P);
-                    } else if constexpr (kHold<S, NV>) {
-#pragma unroll
-                        for (int i = 0; i < NP; ++i) xv[i] = xc[j][i];
                     } else {
                         load_piece<VEC>(x + off + P.col<VEC>(j), xv);
                     }

@@ -281,10 +281,6 @@ __device__ __forceinline__ auto make_feed(uint8_t* ring, int thread_bytes, int G
     else return Feed<S>{ring + 16 * threadIdx.x, thread_bytes * (int)blockDim.x, 0};
 }
 
-// Without a ring (long rows of pairs, with fp32 among them): whether the next row's pieces wait in registers instead.
-template <int S, int NV>
-constexpr bool kHold = S == 0 && NV <= 4;
-
 // ------------------------------------------------------------------ sums over a row
 // Sums of K <= 4 values over the G threads of a row; every thread of the block calls. G < 32: plain
 // shuffles (G a power of two). From a warp up, K values share their shuffles: each exchange halves either the
@@ -467,13 +463,16 @@ inline cudaError_t colsum(const float* part0, float* out0, const float* part1, f
 // Threads and pieces of a row. A piece is 16 bytes of the widest type in the row (8 bf16, or 4 where
 // fp32 stands beside them: with 8 the fp32 accesses of a warp would leave every other 16 bytes out,
 // 305 instead of 212 us for the backward of 16384 x 4096 with an fp32 residual), 4 elements where D is no
-// multiple of 8, then 2, then 1; pairs in an odd row with bf16 (RowFeed), up to 512 threads. A thread
-// holds 16 elements, so that the row sums' exchange and the addresses of a row are spread over many; with narrower
-// pieces 4 of them while 512 threads do. A row has a power of two of lanes up to a warp, whole warps beyond.
+// multiple of 8, then 2, then 1; pairs in an odd row (RowFeed) with bf16, up to 512 threads, and in
+// one of fp32 beyond 2048 elements while two stages fit (16384 x 3001, backward: 310 us, 1706 with single
+// elements). A thread holds 16 elements, so that the row sums' exchange and the addresses of a row are spread
+// over many; with narrower pieces 4 of them while 512 threads do. A row has a power of two of lanes up to a warp,
+// whole warps beyond.
 struct RowPlan {
     int vec, nv, G, threads;
     bool ring;   // pieces of 4 bytes or more in every operand, or rows of a RowFeed; at most 512 threads (kWide)
     bool odd;    // of a RowFeed
+    bool all_f32;
 };
 // wide_rows: 8 elements a thread for 4096 < D <= 6144, where 16 would leave an SM one block of 9 to 12 warps, their
 // registers too many for two. addnorm backward, 16384 x 5120 in bf16: 240 us, 287 with 16 elements; the
@@ -482,7 +481,8 @@ constexpr int kWide = 768;
 inline RowPlan row_plan(int D, bool all_bf16, bool all_f32, bool wide_rows = false) {
     RowPlan p;
     p.vec = all_bf16 && D % 8 == 0 ? 8 : D % 4 == 0 ? 4 : D % 2 == 0 ? 2 : 1;
-    p.odd = D % 2 == 1 && !all_f32 && D <= 512 * kRowElems;
+    p.all_f32 = all_f32;
+    p.odd = D % 2 == 1 && (all_f32 ? D > 2048 && D <= 416 * kRowElems : D <= 512 * kRowElems);
     if (p.odd) p.vec = 2;
     const int nvec = cdiv(D, p.vec);
     const bool wide = wide_rows && p.vec >= 4 && D > 4096 && D <= 8 * kWide;
@@ -495,22 +495,26 @@ inline RowPlan row_plan(int D, bool all_bf16, bool all_f32, bool wide_rows = fal
         for (p.G = 1; p.G < need;) p.G *= 2;
         p.threads = 256;
     }
-    p.ring = p.odd || p.threads <= (wide ? kWide : 512) && (p.vec > 1 || all_f32) && !(p.vec < 4 && p.nv > 4);
+    p.ring = p.odd || p.threads <= (wide ? kWide : 512) && !(p.vec == 1 && p.nv > 4);
     return p;
 }
 // Shared memory in front of the ring: the row sums' buffer; it and the ring are free again when the column
 // sums of a block's row groups need their blockDim * 16 floats at most.
 constexpr int kHead = 1024;
 constexpr int kSmSmem = 220 * 1024;    // of an SM, for its blocks
-// Stages of the ring: 3 where two blocks of them fit an SM, else 2 where one does, else none.
 inline int stage_bytes(const RowPlan& p, int thread_bytes) {
     return p.odd ? thread_bytes / kRowElems * odd_room(p.G) * (p.threads / p.G) : thread_bytes * p.threads;
 }
+// Stages of the ring. 3 where two blocks of them fit an SM; with bf16 in the row only if those are the 14 warps
+// that its arithmetic wants (16384 x 2560 with an fp32 residual, backward: 141 us with 15 warps of 2 stages, 186
+// with 10 of 3), and also where a single block is all that fits with 2 (8192, bf16: 303 and 328 us). Else 2, or
+// none where 2 do not fit.
 inline int ring_stages(const RowPlan& p, int thread_bytes) {
     const int row = stage_bytes(p, thread_bytes);
     if (!p.ring) return 0;
-    if (2 * (3 * row + kHead + 1024) <= kSmSmem) return 3;
-    return 2 * row + kHead + 1024 <= kSmSmem ? 2 : 0;
+    const int n3 = kSmSmem / (3 * row + kHead + 1024), n2 = kSmSmem / (2 * row + kHead + 1024);
+    if (p.all_f32 ? n3 >= 2 : n3 * p.threads >= 448 && (n3 >= 2 || n2 < 2)) return 3;
+    return n2 ? 2 : 0;
 }
 inline size_t block_smem(const RowPlan& p, int stages, int thread_bytes) {
     const size_t ring = kHead + (size_t)stages * stage_bytes(p, thread_bytes);
@@ -557,32 +561,37 @@ template <int V, int N, int S, int M, bool O = false> struct Shape {
 };
 // BF16, F32: every operand of the row has that type, so pieces of 8, and a ring of single elements, exist too.
 // Blocks of up to 256 threads (D <= 4096 with pieces of 4 or 8) have kernels of their own, which need not fit their
-// registers into a larger block's share. Without a ring up to 1024 threads: with 16 elements each they
-// spill; only rows beyond 8192 elements, or too long for two stages.
+// registers into a larger block's share. Without a ring only rows beyond 8192 elements (up to 1024 threads, which
+// with 16 elements each spill), odd fp32 rows beyond 6656, and rows too long for two stages.
 template <int V, int N, int S, bool O = false, typename F>
 cudaError_t by_block(const RowPlan& p, F&& f) {
     return p.threads <= 256 ? f(Shape<V, N, S, 256, O>{}) : f(Shape<V, N, S, 512, O>{});
 }
+template <int V, int N, typename F>
+cudaError_t by_block(const RowPlan& p, F&& f) {   // no ring
+    return p.threads <= 512 ? f(Shape<V, N, 0, 512>{}) : f(Shape<V, N, 0, 1024>{});
+}
 template <bool BF16, bool F32, bool WIDE, typename F>
 cudaError_t by_shape(const RowPlan& p, int stages, F&& f) {
-    if constexpr (!F32)
-        if (p.odd) return stages == 3 ? by_block<2, 8, 3, true>(p, f) : f(Shape<2, 8, 2, 512, true>{});
+    if (p.odd) {
+        if (stages == 2) return f(Shape<2, 8, 2, 512, true>{});
+        if constexpr (F32) return f(Shape<2, 8, 3, 512, true>{});
+        else return by_block<2, 8, 3, true>(p, f);
+    }
     if (p.vec == 1) {
         if constexpr (F32)
             if (p.nv == 4) return by_block<1, 4, 3>(p, f);   // three stages of 512 threads fit twice
-        return f(Shape<1, 16, 0, 1024>{});
+        return by_block<1, 16>(p, f);
     }
     if (p.vec == 2) {
-        if (p.nv == 8) return f(Shape<2, 8, 0, 1024>{});
-        return stages == 3 ? by_block<2, 4, 3>(p, f) : f(Shape<2, 4, 0, 512>{});
+        if (p.nv == 4) return stages == 3 ? by_block<2, 4, 3>(p, f) : f(Shape<2, 4, 2, 512>{});
+        return stages == 3 ? f(Shape<2, 8, 3, 512>{}) : stages == 2 ? f(Shape<2, 8, 2, 512>{}) : by_block<2, 8>(p, f);
     }
     if constexpr (WIDE)
         if (p.vec * p.nv == 8) {
-            if constexpr (BF16) {
+            if constexpr (BF16)
                 if (p.vec == 8) return stages == 3 ? f(Shape<8, 1, 3, kWide>{}) : f(Shape<8, 1, 2, kWide>{});
-                if (stages == 3) return f(Shape<4, 2, 3, kWide>{});
-            }
-            return f(Shape<4, 2, 2, kWide>{});
+            return stages == 3 ? f(Shape<4, 2, 3, kWide>{}) : f(Shape<4, 2, 2, kWide>{});
         }
     if constexpr (BF16)
         if (p.vec == 8)
@@ -591,7 +600,7 @@ cudaError_t by_shape(const RowPlan& p, int stages, F&& f) {
                                  : f(Shape<8, 2, 0, 1024>{});
     return stages == 3   ? by_block<4, 4, 3>(p, f)
            : stages == 2 ? f(Shape<4, 4, 2, 512>{})
-                         : f(Shape<4, 4, 0, 1024>{});
+                         : by_block<4, 4>(p, f);
 }
 template <typename F>
 cudaError_t by_kind(int kind, F&& f) {

@@ -69,7 +69,8 @@ ROWS = [(1, 1), (3, 7), (5, 8), (1, 33), (64, 64), (70, 100), (9, 257), (33, 256
         (5, 2048), (300, 2052), (3, 4096), (4, 4104), (2, 8192), (3, 8200), (2, 9999), (2, 16384),
         (400, 66), (2000, 78), (900, 330), (700, 333), (5, 2050), (3, 4098), (3, 4100), (2, 2049), (900, 1185),
         (301, 17), (70, 101), (2000, 9), (3, 4097), (300, 3001), (5, 8191), (2, 8193),
-        (400, 5120), (9, 6144), (300, 6148), (5, 5004)]
+        (400, 5120), (9, 6144), (300, 6148), (5, 5004), (40, 5002),
+        (3, 8190), (9, 6662), (170, 3333), (40, 6655), (3, 6657), (200, 8192), (200, 2560)]
 
 
 def addnorm_inputs(N, D, io, res, seed):
