@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(MAXT, ODD || (MAXT == 256 && VEC == 8) ? (MAXT
 }
 
 template <typename T, typename R, int VEC, int NV, int S, int KIND, int MAXT, bool ODD>
-__global__ void __launch_bounds__(MAXT < 512 ? 448 : MAXT)   // 144 registers. 16384 x 2048: 78 us; 81 at 512 threads' 128
+__global__ void __launch_bounds__(MAXT < 512 ? 448 : MAXT)   // 144 registers; 16384 x 2048: 78 us, 81 at 128
     k_addnorm_bwd(const T* __restrict__ x, const R* __restrict__ r_in, const float* __restrict__ rscale,
                   const float* __restrict__ w, const T* __restrict__ dy, const R* dr, R* dres, T* __restrict__ dx,
                   float* __restrict__ pdw, float* __restrict__ pds, int rows, int D, int G, float alpha, float eps) {
@@ -335,10 +335,11 @@ gla_status gla_addnorm_bwd(const gla_norm_problem* p, const void* x, const void*
             return by_shape<sizeof(T) + sizeof(R) == 4, sizeof(T) == 4, true>(rp, stages, [&](auto sh) {
                 return by_kind(p->kind, [&](auto kind) {
                     using Sh = decltype(sh);
-                    auto kern = k_addnorm_bwd<T, R, Sh::vec, Sh::nv, Sh::stages, decltype(kind)::value, Sh::maxt, Sh::odd>;
+                    auto kern = k_addnorm_bwd<T, R, Sh::vec, Sh::nv, Sh::stages, decltype(kind)::value, Sh::maxt,
+                                              Sh::odd>;
                     const size_t smem = block_smem(rp, Sh::stages, thread_bytes);
                     static std::atomic<bool> seen[kMaxDevices];
-                static Occupancy known;
+                    static Occupancy known;
                     const cudaError_t e = smem_attr_once(kern, kSmSmem, seen);
                     if (e != cudaSuccess) return e;
                     P = fit_blocks(kern, rp, smem, P, 1, known);

@@ -339,7 +339,7 @@ gla_status gla_headnorm_fwd(const gla_norm_problem* p, const void* o, const void
                                                decltype(act)::value, Sh::maxt, Sh::odd>;
                     const size_t smem = block_smem(rp, Sh::stages, thread_bytes);
                     static std::atomic<bool> seen[kMaxDevices];
-                static Occupancy known;
+                    static Occupancy known;
                     const cudaError_t e = smem_attr_once(kern, kSmSmem, seen);
                     if (e != cudaSuccess) return e;
                     const dim3 grid(fit_blocks(kern, rp, smem, row_blocks(rp, tokens, p->H), p->H, known), p->H);
@@ -383,7 +383,7 @@ gla_status gla_headnorm_bwd(const gla_norm_problem* p, const void* o, const void
                                                    decltype(act)::value, Sh::maxt, Sh::odd>;
                         const size_t smem = block_smem(rp, Sh::stages, thread_bytes);
                         static std::atomic<bool> seen[kMaxDevices];
-                static Occupancy known;
+                        static Occupancy known;
                         const cudaError_t e = smem_attr_once(kern, kSmSmem, seen);
                         if (e != cudaSuccess) return e;
                         P = fit_blocks(kern, rp, smem, P, p->H, known);

@@ -9,10 +9,10 @@
 // share it, 16 elements a thread, so that the row sums' exchange is spread over many elements;
 // arithmetic is on packed pairs of fp32; several sums share their shuffles; and every thread copies its
 // own pieces of the next rows into shared memory asynchronously (a ring that only its own thread
-// reads, so no barrier guards it). Rows of up to 512 elements belong to a warp or less, longer ones to a
+// reads, so no barrier guards it; odd rows share theirs). Rows of up to 512 elements belong to a warp or less, longer ones to a
 // block. Blocks walk many rows and keep the column sums (dw) in registers.
 // Measured, device time and share of the copy rate: addnorm forward 16384 x 4096 (fp32 residual) 133 us
-// (0.92), backward 16384 x 2048 81 us (0.76); headnorm forward 4 x 16 x 4096 x 256 68 us (0.91), backward
+// (0.92), backward 16384 x 2048 79 us (0.78); headnorm forward 4 x 16 x 4096 x 256 68 us (0.91), backward
 // 2 x 8 x 8192 x 256 65 us (0.78).
 #pragma once
 #include <type_traits>

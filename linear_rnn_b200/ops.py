@@ -571,8 +571,8 @@ def gla_addnorm_bwd(x, r, w, dy, dr=None, *, rscale=None, alpha: float = 1.0, ki
         ps = _ptr_of("rscale", rscale, cols, _f32, dev)
         px = _ptr_of("x (for rscale's gradient)", _need("x (for rscale's gradient)", x), shape, dtype, dev)
         ds = torch.empty_like(rscale)
-    ws, pws, nbytes = _partials("gla_addnorm_workspace_bytes", workspace, _lib.lib.gla_addnorm_workspace_bytes(ref), dev,
-                                dy)
+    ws, pws, nbytes = _partials("gla_addnorm_workspace_bytes", workspace, _lib.lib.gla_addnorm_workspace_bytes(ref),
+                                dev, dy)
     dres = torch.empty_like(r)
     dx = torch.empty_like(dy) if output_dx else None
     dw = torch.empty_like(w) if w is not None else None
