@@ -164,12 +164,7 @@ def _own(s, case):
         prob = ops.make_scan_problem(s["x"])
         saved = torch.empty(ops.gla_scan_saved_bytes(prob), dtype=torch.uint8, device=s["x"].device)
         o, hT = ops.gla_scan_fwd(s["x"], s["g"], s["h0"], input=case["input"], saved_states=saved)
-        dhT = s["dhT"]
-        if dhT is not None and s["dO"].dtype == torch.float32:
-            # as in the plain form, an fp32 dO is the buffer that takes the end state's gradient in, on every pass
-            s["dO"].select(2, -1).add_(dhT)
-            dhT = None
-        grads = ops.gla_scan_bwd(s["x"], s["g"], s["h0"], s["dO"], dhT, input=case["input"], saved_states=saved)
+        grads = ops.gla_scan_bwd(s["x"], s["g"], s["h0"], s["dO"], s["dhT"], input=case["input"], saved_states=saved)
         return {"o": o, "hT": hT, **grads}
     if case["op"] == "addnorm":
         if case["pass"] == "fwd":
@@ -230,6 +225,7 @@ def _scan_train(s, case):
     # the gradient of h_t is dO_t + a_{t+1} dh_{t+1}: the same recurrence from the other end
     up = dO.float()
     if s["dhT"] is not None:
+        up = up.clone()       # an fp32 dO is the case's own
         up[:, :, -1] += s["dhT"]
     after = torch.cat([a[:, :, 1:], torch.zeros_like(a[:, :, :1])], 2)
     dh = _linear_scan(after.flip(2), up.flip(2)).flip(2)
