@@ -324,10 +324,13 @@ GLA_API gla_status gla_mlstm_bwd_saved(const gla_problem* p, const void* q, cons
  * p: B, H, L >= 0; at most 2^30 tokens; Dk = Dv = D, the channels per head, 1 <= D <= 65536; io; gate must be
  *   GLA_GATE_PER_KEY; chunk, scale and plan are ignored.
  * x, o, dO, dx [B,H,L,D] in io dtype; g, dg [B,H,L,D] f32; h0, hT, dhT, dh0 [B,H,D] f32.
- * g may be any real (GLA_SCAN_NORM: g <= 0, where m is real; g = 0 there gives m = 0, whose
- *   infinite slope is taken as 0). g = -inf is allowed: alpha = 0, so that token starts anew (a
- *   packed document's first token). NaN and infinities in x, g or h0 spread as the formula says;
- *   0 * inf is NaN, so a non-finite state passes through such a start too.
+ * g may be any real whose alpha is an fp32 number, g <= 88 (GLA_SCAN_NORM: g <= 0, where m is real; g = 0
+ *   there, and |g| < 2^-126, gives m = 0, whose infinite slope is taken as 0). g = -inf is allowed:
+ *   alpha = 0, so that token starts anew (a packed document's first token); so does alpha < 2^-126.
+ *   Products of alphas that leave fp32's range over many tokens do no harm where the states stay
+ *   inside it; what they leave of a state below 2^-126 of its size may count as forgotten, whatever
+ *   growth follows. NaN and infinities in x, g or h0 spread as the formula says, token by token:
+ *   an infinite state stays infinite, and as 0 * inf is NaN, it passes through a start as NaN.
  * Sums run in fp32. Nothing in the library's results depends on timing: the order of each
  * channel's products is fixed by the problem's sizes. No atomics.
  * gla_scan_fwd: o [B,H,L,D] (written) and hT (NULL: not written). L = 0 copies h0 (or zero) to hT.

@@ -247,6 +247,80 @@ struct ScanArgs {
     int L, D, nblk, steps;
 };
 
+// ------------------------------------------------------------------ products that leave fp32's range
+// A composed run multiplies its decays before the state meets them, and their product may be no fp32 number where
+// every state is one: e^(g n) over growing gates is infinite, and 0 times it NaN, while the state stays 0; over
+// strong gates it is 0, and an infinite state would become NaN. Both show: a state that is not finite stays so to the
+// end of a walk. So a walk composes, its end is looked at, and only where that is not finite the tile goes
+// again, with the steps that composition cannot take made token by token from the inputs in global memory (the
+// ring's stage may be free already). The look costs a long walk over clusters 2 % (8 heads x 65536 x 128: 104 us
+// without it, 106 with).
+__device__ __forceinline__ bool is_finite(float v) { return fabsf(v) <= 3.402823466e38f; }
+// In any lane: the warp goes again as one, which spares the branch its bookkeeping.
+__device__ __forceinline__ bool any_not_finite(float v) { return __any_sync(0xffffffffu, !is_finite(v)); }
+
+// The tokens of one channel of a head: v is x (forward: h <- a h + m x) or dO (REV: d <- a (dO + d)), L rows D apart.
+template <bool REV, int IN, typename T>
+struct Tokens {
+    const float* g;
+    const T* v;
+    int D, L;
+    // What the n tokens from t0 on, (A, B) when composed, make of state h. A NaN stays; growth leaves the state 0.
+    __device__ __forceinline__ float step(float A, float B, float h, int t0, int n) const {
+        if (h != h) return h;
+        if (is_finite(B)) {
+            if ((A > 0.f && is_finite(A)) || (A == 0.f && is_finite(h))) return fmaf(A, h, B);
+            if (A > 0.f && h == 0.f) return B;
+        }
+#pragma unroll 1
+        for (int j = 0; j < n; ++j) {
+            const int t = t0 + (REV ? n - 1 - j : j);
+            if (t >= L) continue;
+            uint64_t a, u, inv;
+            gate2(f2(g[(size_t)t * D], 0.f), a, u);
+            const float w = to_f(v[(size_t)t * D]);
+            float a0, b0, none;
+            f2_split(a, a0, none);
+            if (REV) {
+                h = a0 * (w + h);
+            } else {
+                f2_split(times_factor2<IN>(in_factor2<IN>(u, inv), f2(w, 0.f)), b0, none);
+                h = fmaf(a0, h, b0);
+            }
+        }
+        return h;
+    }
+};
+
+// Walks N runs of a channel in a tile (A and B of run r lie at r * CH) from run r0, REV: back from r0 + N - 1, with state
+// h: put(r, h) gets the state entering run r and may write it over the run's B. Returns the state after the runs;
+// kept: the B's, for another walk. walk_by_step is that one; t0 is the tile's first token.
+template <bool REV, int N, typename Put>
+__device__ __forceinline__ float walk_runs(const float* A, const float* B, int r0, float h, float (&kept)[N], Put put) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const int r = REV ? r0 + N - 1 - j : r0 + j;
+        kept[j] = B[r * CH];
+        put(r, h);
+        h = fmaf(A[r * CH], h, kept[j]);
+    }
+    return h;
+}
+template <bool REV, int N, typename Tok, typename Put>
+__device__ __forceinline__ float walk_by_step(const float* A, float* B, int r0, float h, const float (&kept)[N],
+                                              const Tok& tok, int t0, Put put) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) B[(REV ? r0 + N - 1 - j : r0 + j) * CH] = kept[j];
+#pragma unroll 1
+    for (int j = 0; j < N; ++j) {
+        const int r = REV ? r0 + N - 1 - j : r0 + j;
+        const float ra = A[r * CH], rb = B[r * CH];
+        put(r, h);
+        h = tok.step(ra, rb, h, t0 + r * RUN, RUN);
+    }
+    return h;
+}
+
 // Sends (A, B) to every CTA of the cluster, waits for theirs and composes them onto `super` in
 // sequence order (reverse order for REV). Returns the value entering this CTA's tile; `super`
 // becomes the value leaving the row of tiles. Slots are used in turn, two rows of tiles apart: a
@@ -266,6 +340,20 @@ __device__ __forceinline__ float exchange(Tail& sm, int c, float A, float B, int
         if (r == rank) in = super;
         const float2 v = sm.slot[(p * cs + r) * CH + c];
         super = fmaf(v.x, super, v.y);
+    }
+    return in;
+}
+// The same row once more by Tokens::step; t0: the row's first token.
+template <bool REV, typename Tail, typename Tok>
+__device__ __forceinline__ float compose_by_step(const Tail& sm, int c, int cs, int rank, int i, float& super,
+                                                 const Tok& tok, int t0) {
+    float in = super;
+#pragma unroll 1
+    for (int k = 0; k < cs; ++k) {
+        const int r = REV ? cs - 1 - k : k;
+        if (r == rank) in = super;
+        const float2 v = sm.slot[((i & 1) * cs + r) * CH + c];
+        super = tok.step(v.x, v.y, super, t0 + r * TT, TT);
     }
     return in;
 }
@@ -416,10 +504,14 @@ __global__ void __launch_bounds__(NT_F, 2)
         }
     } else if (warp == NW) {
         const bool live = c0 + lane < D;
+        // read for live channels only: the others' states are 0
+        const size_t at = bh * L * D + c0 + lane;
+        const Tokens<false, IN, T> tok{P.g + at, static_cast<const T*>(P.x) + at, D, L};
         float super = P.first && live ? P.first[bh * D + c0 + lane] : 0.f;
         for (int i = 0; i < P.steps; ++i) {
             const int t0 = (i * cs + rank) * TT;
             if (ok) ok = mbar_wait(&sm.sums, i & 1);
+            const float before = super;
             float in = super;
             if (cs > 1) {
                 float tA = 1.f, tB = 0.f;
@@ -431,16 +523,21 @@ __global__ void __launch_bounds__(NT_F, 2)
                 }
                 in = exchange<false>(sm, lane, tA, tB, cs, rank, i, super, ok);
             }
-            float h = in;
-#pragma unroll
-            for (int r = 0; r < RUNS; ++r) {
-                sm.start[r][lane] = h;
+            auto put = [&](int r, float v) {
+                sm.start[r][lane] = v;
                 const int t = t0 + r * RUN;
                 if (r * RUN % kSaveEvery == 0 && P.saved && t < L && live)
-                    P.saved[(bh * cdiv(L, kSaveEvery) + t / kSaveEvery) * D + c0 + lane] = h;
-                h = fmaf(sm.A[r][lane], h, sm.B[r][lane]);
-            }
+                    P.saved[(bh * cdiv(L, kSaveEvery) + t / kSaveEvery) * D + c0 + lane] = v;
+            };
+            float kept[RUNS];
+            float h = walk_runs<false>(&sm.A[0][lane], &sm.B[0][lane], 0, in, kept, put);
             if (cs == 1) super = h;
+            if (any_not_finite(super)) {
+                super = in = before;
+                if (cs > 1) in = compose_by_step<false>(sm, lane, cs, rank, i, super, tok, i * cs * TT);
+                h = walk_by_step<false>(&sm.A[0][lane], &sm.B[0][lane], 0, in, kept, tok, t0, put);
+                if (cs == 1) super = h;
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.starts);
         }
@@ -631,6 +728,9 @@ __global__ void __launch_bounds__(NT_F, 2)
         const bool live = c0 + lane < D;
         const size_t ns = cdiv(L, kSaveEvery);
         constexpr int NS = TT / kSaveEvery;   // saved states of a tile
+        const size_t at = bh * L * D + c0 + lane;
+        const Tokens<true, IN, T> back{P.g + at, static_cast<const T*>(P.dO) + at, D, L};
+        const Tokens<false, IN, T> tok{P.g + at, static_cast<const T*>(P.x) + at, D, L};
         float super = P.first && live ? P.first[bh * D + c0 + lane] : 0.f;
         for (int i = 0; i < P.steps; ++i) {
             const int t0 = first_token(i);
@@ -641,6 +741,7 @@ __global__ void __launch_bounds__(NT_F, 2)
                 sv[n] = t < L && live ? P.saved[(bh * ns + t / kSaveEvery) * D + c0 + lane] : 0.f;
             }
             if (ok) ok = mbar_wait(&sm.sums, i & 1);
+            const float before = super;
             float in = super;
             if (cs > 1) {
                 float tA = 1.f, tR = 0.f;
@@ -652,20 +753,26 @@ __global__ void __launch_bounds__(NT_F, 2)
                 }
                 in = exchange<true>(sm, lane, tA, tR, cs, rank, i, super, ok);
             }
-            float h = 0.f, d = in;
-#pragma unroll
-            for (int r = RUNS - 1; r >= 0; --r) {
-                const float rr = sm.R[r][lane];
-                sm.R[r][lane] = d;
-                d = fmaf(sm.A[r][lane], d, rr);
+            {
+                auto put = [&](int r, float v) { sm.R[r][lane] = v; };
+                float kept[RUNS];
+                float d = walk_runs<true>(&sm.A[0][lane], &sm.R[0][lane], 0, in, kept, put);
+                if (cs == 1) super = d;
+                if (any_not_finite(super)) {
+                    super = in = before;
+                    if (cs > 1) in = compose_by_step<true>(sm, lane, cs, rank, i, super, back, t0 - rank * TT);
+                    d = walk_by_step<true>(&sm.A[0][lane], &sm.R[0][lane], 0, in, kept, back, t0, put);
+                    if (cs == 1) super = d;
+                }
             }
-            if (cs == 1) super = d;
 #pragma unroll
-            for (int r = 0; r < RUNS; ++r) {
-                if (r * RUN % kSaveEvery == 0) h = sv[r * RUN / kSaveEvery];
-                const float rb = sm.B[r][lane];
-                sm.B[r][lane] = h;
-                h = fmaf(sm.A[r][lane], h, rb);
+            for (int n = 0; n < NS; ++n) {
+                constexpr int N = RUNS / NS;
+                auto put = [&](int r, float v) { sm.B[r][lane] = v; };
+                float kept[N];
+                float h = walk_runs<false>(&sm.A[0][lane], &sm.B[0][lane], n * N, sv[n], kept, put);
+                if (any_not_finite(h))
+                    walk_by_step<false>(&sm.A[0][lane], &sm.B[0][lane], n * N, sv[n], kept, tok, t0, put);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.starts);
