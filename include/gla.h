@@ -342,7 +342,8 @@ GLA_API gla_status gla_mlstm_bwd_saved(const gla_problem* p, const void* q, cons
  *   gla_scan_fwd_save with the same problem, input and x, g, h0; NULL means recompute (the same
  *   as gla_scan_bwd).
  * ws: the backward's caller-owned device workspace of gla_scan_bwd_workspace_bytes(p) bytes (0 when p
- *   is invalid or unsupported), for the states; with `saved` none is needed (NULL, 0). There is
+ *   is invalid or unsupported), for the states; with `saved`, or without tokens, none is needed
+ *   (NULL, 0; `saved` of 0 bytes may be NULL). There is
  *   no device status word; the kernels' waits on their own copies are bounded, and one that
  *   gave up (a fault elsewhere on the device) ends the call with results that are not valid
  *   rather than hanging.

@@ -292,9 +292,9 @@ struct Tokens {
     }
 };
 
-// Walks N runs of a channel in a tile (A and B of run r lie at r * CH) from run r0, REV: back from r0 + N - 1, with state
-// h: put(r, h) gets the state entering run r and may write it over the run's B. Returns the state after the runs;
-// kept: the B's, for another walk. walk_by_step is that one; t0 is the tile's first token.
+// Walks N runs of a channel in a tile (A and B of run r lie at r * CH) from run r0, REV: back from r0 + N - 1, with
+// state h: put(r, h) gets the state entering run r and may write it over the run's B. Returns the state after the
+// runs; kept: the B's, for another walk. walk_by_step is that one; t0 is the tile's first token.
 template <bool REV, int N, typename Put>
 __device__ __forceinline__ float walk_runs(const float* A, const float* B, int r0, float h, float (&kept)[N], Put put) {
 #pragma unroll
@@ -1133,16 +1133,18 @@ gla_status gla_scan_bwd_saved(const gla_problem* p, int input, const void* x, co
                               void* ws, size_t ws_bytes, void* stream) {
     const gla_status s = check(p);
     if (s != GLA_OK) return s;
-    if (!input_ok(input) || (!saved && !ws)) return GLA_ERR_INVALID_ARG;
+    // no states are needed, saved or recomputed, where there are no tokens: an empty buffer's address may be null
+    const bool recompute = !saved && gla_scan_saved_bytes(p) > 0;
+    if (!input_ok(input) || (recompute && !ws)) return GLA_ERR_INVALID_ARG;
     const bool empty = (size_t)p->B * p->H * p->L == 0;
     if (!empty && (!x || !g || !dO || !dx || !dg)) return GLA_ERR_INVALID_ARG;
     const void* ptrs[] = {x, g, h0, dO, dhT, saved, dx, dg, dh0, ws};
     for (const void* q : ptrs)
         if (!aligned16(q)) return GLA_ERR_INVALID_ARG;
-    if (!saved && ws_bytes < gla_scan_bwd_workspace_bytes(p)) return GLA_ERR_WORKSPACE;
+    if (recompute && ws_bytes < gla_scan_bwd_workspace_bytes(p)) return GLA_ERR_WORKSPACE;
     if ((size_t)p->B * p->H == 0) return GLA_OK;
     cudaStream_t st = (cudaStream_t)stream;
-    if (!saved) {
+    if (recompute) {
         float* own = static_cast<float*>(ws);
         const cudaError_t e = fwd(p, input, x, g, h0, nullptr, nullptr, own, st);
         if (e != cudaSuccess) return record_cuda(e, "scan states");
