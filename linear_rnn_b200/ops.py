@@ -471,11 +471,12 @@ def gla_scan_bwd(x, g, h0, dO, dhT=None, *, input: str = "plain", output_dh0: bo
 
 def gla_scan_decode(x, g, state, *, input: str = "plain") -> torch.Tensor:
     """One token of gla_scan_fwd per (b, h) from `state` (fp32 [B,H,D] on the GPU, updated in
-    place): x, g [B,H,1,D]. Returns o [B,H,1,D]."""
+    place): x, g [B,H,1,D]. Returns o [B,H,1,D], on the GPU. x and g may be on the host; then the call waits for
+    their copies, so that their buffers may be written again when it returns."""
     if not state.is_cuda or state.dtype is not _f32 or not state.is_contiguous():
         raise ValueError("state must be a contiguous float32 CUDA tensor (it is updated in place)")
     if not x.is_cuda or not _need("g", g).is_cuda:
-        x, g = (t.contiguous().to(state.device, non_blocking=True) for t in (x, _need("g", g)))
+        x, g = (t.contiguous().to(state.device) for t in (x, _need("g", g)))
     shape, dtype, dev = x.shape, x.dtype, state.get_device()
     _, ref = _descriptor((shape, dtype), lambda: make_scan_problem(x))
     if shape[2] != 1:
