@@ -303,7 +303,9 @@ def gla_deltanet_bwd(q, k, v, beta, h0, dO, dhT=None, *, scale: Optional[float] 
 # The operators below are also called where a pass takes a few microseconds on the GPU, so their
 # host work is kept short: descriptors are looked up by sizes and types, and every tensor is
 # checked once.
-_getDevice, _rawStream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+# torch's own short cuts for the current device and stream, where it has them (a build without CUDA does not)
+_getDevice = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_rawStream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 _f32 = torch.float32
 
 
