@@ -390,11 +390,18 @@ def _descriptor(key, make):
     return d
 
 
+def _sizes(where, *sizes):
+    """The sizes of a descriptor, whose fields have 32 bits."""
+    if max(sizes) > 2147483647:
+        raise GlaError(_lib.GLA_ERR_UNSUPPORTED, where)
+    return sizes
+
+
 def make_scan_problem(x: torch.Tensor) -> GlaProblem:
     """The gla_problem of the vector-state recurrence over x [B,H,L,D]."""
     if x.dim() != 4:
         raise ValueError("x must be [B, H, L, D]")
-    B, H, L, D = x.shape
+    B, H, L, D = _sizes("x's sizes", *x.shape)
     return GlaProblem(B, H, L, D, D, 64, 1.0, _io_dtype(x.dtype), _lib.GLA_GATE_PER_KEY, _lib.GLA_PLAN_AUTO)
 
 
@@ -498,9 +505,7 @@ def _addnorm_problem(x, res_dtype, kind, eps, alpha) -> GlaNormProblem:
     D = x.shape[-1]
     if D < 1:
         raise ValueError("x must have channels")
-    rows = x.numel() // D
-    if rows > 2147483647:
-        raise GlaError(_lib.GLA_ERR_UNSUPPORTED, "rows")
+    rows, D = _sizes("rows and channels", x.numel() // D, D)
     return GlaNormProblem(1, 1, rows, D, _io_dtype(x.dtype), _io_dtype(res_dtype), _choice("kind", kind, _NORM_KINDS),
                           _lib.GLA_ACT_SILU, 0, eps, alpha)
 
@@ -588,7 +593,7 @@ def gla_addnorm_bwd(x, r, w, dy, dr=None, *, rscale=None, alpha: float = 1.0, ki
 def _headnorm_problem(o, w, act, kind, eps) -> GlaNormProblem:
     if o.dim() != 4:
         raise ValueError("o must be [B, H, L, D]")
-    B, H, L, D = o.shape
+    B, H, L, D = _sizes("o's sizes", *o.shape)
     io = _io_dtype(o.dtype)
     return GlaNormProblem(B, H, L, D, io, io, _choice("kind", kind, _NORM_KINDS), _choice("act", act, _ACTS),
                           1 if w is not None and w.dim() == 2 else 0, eps, 1.0)
