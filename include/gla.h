@@ -343,10 +343,10 @@ GLA_API gla_status gla_mlstm_bwd_saved(const gla_problem* p, const void* q, cons
  *   as gla_scan_bwd).
  * ws: the backward's caller-owned device workspace of gla_scan_bwd_workspace_bytes(p) bytes (0 when p
  *   is invalid or unsupported), for the states; with `saved`, or without tokens, none is needed
- *   (NULL, 0; `saved` of 0 bytes may be NULL). There is
- *   no device status word; the kernels' waits on their own copies are bounded, and one that
- *   gave up (a fault elsewhere on the device) ends the call with results that are not valid
- *   rather than hanging.
+ *   (NULL, 0; `saved` of 0 bytes may be NULL). The
+ *   kernels' waits on their own copies are bounded, and one that gave up (a fault elsewhere on
+ *   the device) ends the call with results that are not valid rather than hanging, which
+ *   gla_scan_check_device_status then reports.
  * Outputs may not overlap inputs, saved or ws. All pointers 16-byte aligned device memory.
  * Errors: GLA_ERR_INVALID_ARG (null or misaligned pointer, bad enum, sizes, a gate mode),
  *   GLA_ERR_UNSUPPORTED (D, L, B * H), GLA_ERR_WORKSPACE, GLA_ERR_CUDA. */
@@ -375,6 +375,12 @@ GLA_API gla_status gla_scan_bwd_saved(const gla_problem* p, int input, const voi
  * token with h0 = state. No workspace. Errors: as gla_scan_fwd. */
 GLA_API gla_status gla_scan_decode(const gla_problem* p, int input, const void* x, const float* g, float* state,
                                    void* o, void* stream);
+
+/* Synchronises `stream`, then reads and clears the status word that the calls of gla_scan_fwd,
+ * gla_scan_bwd and their training pair on the current device share: GLA_OK; GLA_ERR_TIMEOUT when a
+ * bounded device-side wait gave up in one of them since the last check (in any stream or host
+ * thread); GLA_ERR_CUDA if the synchronisation itself failed. The word belongs to the library. */
+GLA_API gla_status gla_scan_check_device_status(void* stream);
 
 /* The norms before and after a block. */
 typedef enum {
@@ -503,6 +509,10 @@ GLA_API gla_status gla_fwd_static_scratch(const gla_problem* p, const void* q, c
  * stays usable. Nothing faults, traps or hangs. Errors: GLA_ERR_INVALID_ARG (before any
  * launch), GLA_ERR_CUDA. */
 GLA_API gla_status gla_debug_wait_timeout(void* ws, unsigned polls, void* stream);
+
+/* The same for gla_scan_*: two of its waits that nothing completes give up after `polls` polls.
+ * gla_scan_check_device_status(stream) then returns GLA_ERR_TIMEOUT once. Errors as above. */
+GLA_API gla_status gla_debug_scan_wait_timeout(unsigned polls, void* stream);
 
 /* Measurement support (not needed for computing).
  * gla_launch_count: number of kernels this process has launched through the library.

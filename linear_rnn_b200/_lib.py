@@ -30,7 +30,8 @@ EXPORTED = ("gla_workspace_bytes", "gla_fwd", "gla_bwd", "gla_status_string",
             "gla_deltanet_bwd_saved", "gla_mlstm_saved_bytes", "gla_mlstm_fwd_save", "gla_mlstm_bwd_saved",
             "gla_scan_bwd_workspace_bytes", "gla_scan_saved_bytes", "gla_scan_fwd", "gla_scan_bwd", "gla_scan_fwd_save",
             "gla_scan_bwd_saved", "gla_scan_decode", "gla_addnorm_workspace_bytes", "gla_addnorm_fwd",
-            "gla_addnorm_bwd", "gla_headnorm_workspace_bytes", "gla_headnorm_fwd", "gla_headnorm_bwd")
+            "gla_addnorm_bwd", "gla_headnorm_workspace_bytes", "gla_headnorm_fwd", "gla_headnorm_bwd",
+            "gla_scan_check_device_status", "gla_debug_scan_wait_timeout")
 
 
 class GlaProblem(ctypes.Structure):
@@ -131,6 +132,10 @@ def _load():
     lib.gla_scan_fwd_save.argtypes = [pp, ctypes.c_int] + [ctypes.c_void_p] * 7
     lib.gla_scan_bwd_saved.argtypes = [pp, ctypes.c_int] + [ctypes.c_void_p] * 10 + [ctypes.c_size_t, ctypes.c_void_p]
     lib.gla_scan_decode.argtypes = [pp, ctypes.c_int] + [ctypes.c_void_p] * 5
+    lib.gla_scan_check_device_status.argtypes = [ctypes.c_void_p]
+    lib.gla_scan_check_device_status.restype = ctypes.c_int
+    lib.gla_debug_scan_wait_timeout.argtypes = [ctypes.c_uint, ctypes.c_void_p]
+    lib.gla_debug_scan_wait_timeout.restype = ctypes.c_int
     lib.gla_addnorm_workspace_bytes.argtypes = [np_]
     lib.gla_addnorm_workspace_bytes.restype = ctypes.c_size_t
     lib.gla_addnorm_fwd.argtypes = [np_] + [ctypes.c_void_p] * 7

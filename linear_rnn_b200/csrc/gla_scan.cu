@@ -235,6 +235,22 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     return r;
 }
 
+// ------------------------------------------------------------------ waits that may give up
+__device__ int scan_status;   // kDevStatus bits of the device's calls since gla_scan_check_device_status last read them
+
+// A thread whose wait gave up waits no more: it runs the walk out, sends nothing to other CTAs, and says so here at the
+// end. The threads do not tell each other on the way: looking for that at every wait cost the training pair 4 %.
+__device__ __forceinline__ void report(bool ok) {
+    if (!ok) atomicOr(&scan_status, kDevStatusTimeout);
+}
+
+// Waits for the last copies of a ring that n loads have gone through, one barrier a stage: none may be on its way when
+// the CTA's shared memory is given up, whatever the walk came to.
+template <int S>
+__device__ __forceinline__ void land(uint64_t (&full)[S], int n) {
+    for (int i = n < S ? 0 : n - S; i < n; ++i) mbar_wait(&full[i % S], (i / S) & 1);
+}
+
 struct ScanArgs {
     const void* x;
     const float* g;
@@ -331,8 +347,8 @@ __device__ __forceinline__ float exchange(Tail& sm, int c, float A, float B, int
                                           float& super, bool& ok) {
     float in = super;
     const int p = i & 1;
-    if (c == 0) mbar_arrive_expect_tx(&sm.got[p], cs * CH * (uint32_t)sizeof(float2));
-    for (int r = 0; r < cs; ++r)
+    if (c == 0 && ok) mbar_arrive_expect_tx(&sm.got[p], cs * CH * (uint32_t)sizeof(float2));
+    for (int r = 0; r < cs && ok; ++r)   // nothing more is sent after a wait that gave up
         st_async_pair(mapa_shared(&sm.slot[(p * cs + rank) * CH + c], r), mapa_shared(&sm.got[p], r), A, B);
     if (ok) ok = mbar_wait_cluster(&sm.got[p], (i >> 1) & 1);
     for (int k = 0; k < cs; ++k) {
@@ -543,15 +559,18 @@ __global__ void __launch_bounds__(NT_F, 2)
         }
         if (P.last && rank == 0 && live) P.last[bh * D + c0 + lane] = super;
     } else if (LOAD == LOAD_TMA && lane == 0) {
-        for (int i = 0; i < P.steps; ++i) {
+        int i = 0;
+        for (; i < P.steps; ++i) {
             const int s = i % kFwdStages, t0 = (i * cs + rank) * TT;
             float* sg = reinterpret_cast<float*>(smem + s * kStage);
-            if (i >= kFwdStages && ok) ok = mbar_wait(&sm.empty[s], (i / kFwdStages - 1) & 1);
+            if (i >= kFwdStages && !(ok = mbar_wait(&sm.empty[s], (i / kFwdStages - 1) & 1))) break;
             mbar_arrive_expect_tx(&sm.full[s], kStage);
             tma_load_3d(sg, &mg, c0, t0, (int)bh, &sm.full[s]);
             tma_load_3d(sg + ELEMS, &mx, c0, t0, (int)bh, &sm.full[s]);
         }
+        land(sm.full, i);
     }
+    report(ok);
     __syncwarp();
     if (cs > 1) cluster_sync();   // no CTA leaves while another may still write to its slots
 }
@@ -779,17 +798,20 @@ __global__ void __launch_bounds__(NT_F, 2)
         }
         if (P.last && rank == 0 && live) P.last[bh * D + c0 + lane] = super;
     } else if (LOAD == LOAD_TMA && lane == 0) {
-        for (int i = 0; i < P.steps; ++i) {
+        int i = 0;
+        for (; i < P.steps; ++i) {
             const int s = i % S, t0 = first_token(i);
             float* sg = reinterpret_cast<float*>(smem + s * kStage);
             T* sx = reinterpret_cast<T*>(sg + ELEMS);
-            if (i >= S && ok) ok = mbar_wait(&sm.empty[s], (i / S - 1) & 1);
+            if (i >= S && !(ok = mbar_wait(&sm.empty[s], (i / S - 1) & 1))) break;
             mbar_arrive_expect_tx(&sm.full[s], kStage);
             tma_load_3d(sg, &mg, c0, t0, (int)bh, &sm.full[s]);
             tma_load_3d(sx, &mx, c0, t0, (int)bh, &sm.full[s]);
             tma_load_3d(sx + ELEMS, &md, c0, t0, (int)bh, &sm.full[s]);
         }
+        land(sm.full, i);
     }
+    report(ok);
     __syncwarp();
     if (cs > 1) cluster_sync();
 }
@@ -926,6 +948,20 @@ __global__ void __launch_bounds__(NT_D) k_scan_decode(const T* __restrict__ x, c
         put4<1>(state + i, h, 0, (int)(n - i));
         put4<1>(o + i, h, 0, (int)(n - i));
     }
+}
+
+// Waits that nothing completes, one of each kind, which give up after `polls` polls.
+__global__ void __launch_bounds__(64) k_scan_wait_timeout(uint32_t polls) {
+    __shared__ __align__(8) uint64_t bar;
+    if (threadIdx.x == 0) {
+        mbar_init(&bar, 1);
+        mbar_fence_init();
+    }
+    __syncthreads();
+    bool ok = true;
+    if (threadIdx.x == 0) ok = mbar_wait(&bar, 0, polls);
+    if (threadIdx.x == 32) ok = mbar_wait_cluster(&bar, 0, polls);
+    report(ok);
 }
 
 // Calls f(T{}, integral_constant<IN>) for the problem's dtype and input factor.
@@ -1179,6 +1215,27 @@ gla_status gla_scan_decode(const gla_problem* p, int input, const void* x, const
         return cudaGetLastError();
     });
     return record_cuda(e, "scan decode");
+}
+
+gla_status gla_scan_check_device_status(void* stream) {
+    cudaStream_t st = (cudaStream_t)stream;
+    int word = 0;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(&word, scan_status, sizeof(int), 0, cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    if (e == cudaSuccess && word != kDevStatusOk) {
+        const int none = kDevStatusOk;
+        e = cudaMemcpyToSymbolAsync(scan_status, &none, sizeof(int), 0, cudaMemcpyHostToDevice, st);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    }
+    if (e != cudaSuccess) return record_cuda(e, "scan status");
+    return word == kDevStatusOk ? GLA_OK : GLA_ERR_TIMEOUT;
+}
+
+gla_status gla_debug_scan_wait_timeout(unsigned polls, void* stream) {
+    if (polls == 0 || polls > kWaitPolls) return GLA_ERR_INVALID_ARG;
+    cudaStream_t st = (cudaStream_t)stream;
+    GLA_LAUNCH("debug_scan_wait_timeout", st, (k_scan_wait_timeout<<<1, 64, 0, st>>>(polls)));
+    return record_cuda(cudaGetLastError(), "scan wait-timeout kernel launch");
 }
 
 }  // extern "C"

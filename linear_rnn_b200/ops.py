@@ -499,6 +499,13 @@ def gla_scan_decode(x, g, state, *, input: str = "plain") -> torch.Tensor:
     return o
 
 
+def gla_scan_check_device_status(device=None) -> int:
+    """Waits for the current stream of `device` (None: the current one) and returns the status of the gla_scan_* calls on
+    it since the last check: GLA_OK, or GLA_ERR_TIMEOUT where a bounded wait on the GPU gave up."""
+    with torch.cuda.device(device):
+        return int(_lib.lib.gla_scan_check_device_status(_rawStream(_getDevice())))
+
+
 def _addnorm_problem(x, res_dtype, kind, eps, alpha) -> GlaNormProblem:
     if x.dim() < 1:
         raise ValueError("x must be [..., D]")

@@ -24,3 +24,8 @@ def test_with_tokens_the_states_or_a_workspace_are_needed():
     fn = _lib.lib.gla_scan_bwd_saved
     assert fn(ctypes.byref(p), 0, *args(None, None), 0, None) == _lib.GLA_ERR_INVALID_ARG
     assert fn(ctypes.byref(p), 0, *args(None, ctypes.c_void_p(16)), 16, None) == _lib.GLA_ERR_WORKSPACE
+
+
+def test_the_wait_diagnostic_validates_before_launch():
+    for polls in (0, (1 << 20) + 1):
+        assert _lib.lib.gla_debug_scan_wait_timeout(polls, None) == _lib.GLA_ERR_INVALID_ARG
