@@ -96,8 +96,15 @@ __global__ void __launch_bounds__(MAXT, ODD || (MAXT == 256 && VEC == 8) ? (MAXT
     }
 }
 
+// The kernels of blocks of up to 256 threads, which the bound in their launch bounds tunes: 448 and 512 threads both leave
+// a thread 128 registers (14 warps too are four to one of the schedulers), spent in another order. us at 512 and at
+// 448, 16384 rows: all in bf16, RMS x 768 38 / 43, x 2048 73 / 85, x 4096 136 / 158, layer x 768 44 / 44, x 2048 80 / 79,
+// x 4096 151 / 148; fp32 x 2048 RMS 132 / 143, layer 149 / 140; fp32 residual, layer x 3000 187 / 210 (60 bytes of
+// spills); pairs, RMS x 2002 121 / 115.
+template <typename T, int VEC, int KIND>
+constexpr int bwd_bound = VEC >= 4 && (KIND == GLA_NORM_RMS || (VEC == 4 && sizeof(T) == 2)) ? 512 : 448;
 template <typename T, typename R, int VEC, int NV, int S, int KIND, int MAXT, bool ODD>
-__global__ void __launch_bounds__(MAXT < 512 ? 448 : MAXT)   // 144 registers; 16384 x 2048: 78 us, 81 at 128
+__global__ void __launch_bounds__(MAXT >= 512 ? MAXT : bwd_bound<T, VEC, KIND>)
     k_addnorm_bwd(const T* __restrict__ x, const R* __restrict__ r_in, const float* __restrict__ rscale,
                   const float* __restrict__ w, const T* __restrict__ dy, const R* dr, R* dres, T* __restrict__ dx,
                   float* __restrict__ pdw, float* __restrict__ pds, int rows, int D, int G, float alpha, float eps) {
@@ -284,7 +291,7 @@ gla_status gla_addnorm_fwd(const gla_norm_problem* p, const void* x, const void*
         using T = decltype(tv);
         using R = decltype(rv);
         const int thread_bytes = rp.nv * rp.vec * (int)(sizeof(T) + sizeof(R));
-        const int stages = ring_stages(rp, thread_bytes);
+        const int stages = ring_stages(rp, thread_bytes, p->kind);
         return by_shape<sizeof(T) + sizeof(R) == 4, sizeof(T) == 4, false>(rp, stages, [&](auto sh) {
             return by_kind(p->kind, [&](auto kind) {
                 using Sh = decltype(sh);
@@ -331,7 +338,7 @@ gla_status gla_addnorm_bwd(const gla_norm_problem* p, const void* x, const void*
             using T = decltype(tv);
             using R = decltype(rv);
             const int thread_bytes = 2 * rp.nv * rp.vec * (int)(sizeof(T) + sizeof(R));
-            const int stages = ring_stages(rp, thread_bytes);
+            const int stages = ring_stages(rp, thread_bytes, p->kind);
             return by_shape<sizeof(T) + sizeof(R) == 4, sizeof(T) == 4, true>(rp, stages, [&](auto sh) {
                 return by_kind(p->kind, [&](auto kind) {
                     using Sh = decltype(sh);

@@ -331,7 +331,7 @@ gla_status gla_headnorm_fwd(const gla_norm_problem* p, const void* o, const void
     const cudaError_t e = by_io(p->io, [&](auto tv) {
         using T = decltype(tv);
         const int thread_bytes = 2 * rp.nv * rp.vec * (int)sizeof(T);
-        return by_shape<sizeof(T) == 2, sizeof(T) == 4, false>(rp, ring_stages(rp, thread_bytes), [&](auto sh) {
+        return by_shape<sizeof(T) == 2, sizeof(T) == 4, false>(rp, ring_stages(rp, thread_bytes, p->kind), [&](auto sh) {
             return by_kind(p->kind, [&](auto kind) {
                 return by_act(p->act, [&](auto act) {
                     using Sh = decltype(sh);
@@ -375,7 +375,7 @@ gla_status gla_headnorm_bwd(const gla_norm_problem* p, const void* o, const void
         e = by_io(p->io, [&](auto tv) {
             using T = decltype(tv);
             const int thread_bytes = 3 * rp.nv * rp.vec * (int)sizeof(T);
-            return by_shape<sizeof(T) == 2, sizeof(T) == 4, false>(rp, ring_stages(rp, thread_bytes), [&](auto sh) {
+            return by_shape<sizeof(T) == 2, sizeof(T) == 4, false>(rp, ring_stages(rp, thread_bytes, p->kind), [&](auto sh) {
                 return by_kind(p->kind, [&](auto kind) {
                     return by_act(p->act, [&](auto act) {
                         using Sh = decltype(sh);

@@ -505,15 +505,20 @@ constexpr int kSmSmem = 220 * 1024;    // of an SM, for its blocks
 inline int stage_bytes(const RowPlan& p, int thread_bytes) {
     return p.odd ? thread_bytes / kRowElems * odd_room(p.G) * (p.threads / p.G) : thread_bytes * p.threads;
 }
-// Stages of the ring. 3 where two blocks of them fit an SM; with bf16 in the row only if those are the 14 warps
-// that its arithmetic wants (16384 x 2560 with an fp32 residual, backward: 141 us with 15 warps of 2 stages, 186
-// with 10 of 3), and also where a single block is all that fits with 2 (8192, bf16: 303 and 328 us). Else 2, or
-// none where 2 do not fit.
-inline int ring_stages(const RowPlan& p, int thread_bytes) {
+// Stages of the ring: 3 or 2, or none where 2 do not fit. fp32 alone: 3 where two blocks of them fit an SM. With bf16 in
+// the row the arithmetic wants 14 warps: 3 where they have them, or 2 would not bring more blocks (512 threads fill
+// the registers at 128 each), or a single block is all that fits with 2. 16384 rows backward with an fp32 residual,
+// layer norm, us with 3 and with 2 stages: x 2048 122 / 108, x 2560 174 / 140, x 3000 187 / 200; 8192 in bf16 303 / 328.
+// The RMS norm, of less arithmetic, keeps 3 in blocks of up to 128 threads too: x 1280 72 / 78, x 2048 101 / 106, but
+// x 2560 137 / 132, and odd rows x 1001 113 / 92.
+inline int ring_stages(const RowPlan& p, int thread_bytes, int kind) {
     const int row = stage_bytes(p, thread_bytes);
     if (!p.ring) return 0;
     const int n3 = kSmSmem / (3 * row + kHead + 1024), n2 = kSmSmem / (2 * row + kHead + 1024);
-    if (p.all_f32 ? n3 >= 2 : n3 * p.threads >= 448 && (n3 >= 2 || n2 < 2)) return 3;
+    if (n3 >= 2 && (p.all_f32 || n3 * p.threads >= 448 || n3 >= (n2 < 512 / p.threads ? n2 : 512 / p.threads) ||
+                    (kind == GLA_NORM_RMS && p.threads <= 128 && !p.odd)))
+        return 3;
+    if (!p.all_f32 && n2 < 2 && n3 * p.threads >= 448) return 3;
     return n2 ? 2 : 0;
 }
 inline size_t block_smem(const RowPlan& p, int stages, int thread_bytes) {
