@@ -36,9 +36,18 @@ __device__ __forceinline__ void act_grad2(uint64_t z, uint64_t& f, uint64_t& df)
     float u0, u1;
     f2_split(f2_add(e, f2_all(1.f)), u0, u1);
     const uint64_t p = f2(tc::rcp_approx(u0), tc::rcp_approx(u1));   // 0 where e is infinite
-    const uint64_t q = f2_fma(p, f2_all(-1.f), f2_all(1.f));
-    f = ACT == GLA_ACT_SILU ? f2_mul(z, p) : p;
-    df = ACT == GLA_ACT_SILU ? f2_mul(p, f2_fma(z, q, f2_all(1.f))) : f2_mul(p, q);
+    if (ACT == GLA_ACT_SILU) {
+        const uint64_t q = f2_fma(p, f2_all(-1.f), f2_all(1.f));   // next to z q of 1 + z q its rounding is small
+        f = f2_mul(z, p);
+        df = f2_mul(p, f2_fma(z, q, f2_all(1.f)));
+    } else {
+        // 1 - p as e p keeps its digits where p is near 1 (at z = 15 the difference is off by a fifth); where e is
+        // infinite the product is NaN and the minimum 1
+        float q0, q1;
+        f2_split(f2_mul(e, p), q0, q1);
+        f = p;
+        df = f2_mul(p, f2(fminf(q0, 1.f), fminf(q1, 1.f)));
+    }
 }
 
 // The tokens of one head that a thread's group takes, one every `step`: element offsets of the token in
