@@ -96,11 +96,11 @@ __global__ void __launch_bounds__(MAXT, ODD || (MAXT == 256 && VEC == 8) ? (MAXT
     }
 }
 
-// The kernels of blocks of up to 256 threads, which the bound in their launch bounds tunes: 448 and 512 threads both leave
-// a thread 128 registers (14 warps too are four to one of the schedulers), spent in another order. us at 512 and at
-// 448, 16384 rows: all in bf16, RMS x 768 38 / 43, x 2048 73 / 85, x 4096 136 / 158, layer x 768 44 / 44, x 2048 80 / 79,
-// x 4096 151 / 148; fp32 x 2048 RMS 132 / 143, layer 149 / 140; fp32 residual, layer x 3000 187 / 210 (60 bytes of
-// spills); pairs, RMS x 2002 121 / 115.
+// The kernels of blocks of up to 256 threads, which the bound in their launch bounds tunes: 448 and 512 threads both
+// leave a thread 128 registers (14 warps too are four to one of the schedulers), spent in another order. us at 512 and
+// at 448, 16384 rows: all in bf16, RMS x 768 38 / 43, x 2048 73 / 85, x 4096 136 / 158, layer x 768 44 / 44, x 2048
+// 80 / 79, x 4096 151 / 148; fp32 x 2048 RMS 132 / 143, layer 149 / 140; fp32 residual, layer x 3000 187 / 210 (60
+// bytes of spills); pairs, RMS x 2002 121 / 115.
 template <typename T, int VEC, int KIND>
 constexpr int bwd_bound = VEC >= 4 && (KIND == GLA_NORM_RMS || (VEC == 4 && sizeof(T) == 2)) ? 512 : 448;
 template <typename T, typename R, int VEC, int NV, int S, int KIND, int MAXT, bool ODD>

@@ -8,12 +8,7 @@ namespace gla {
 namespace {
 
 using namespace norm;
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
+using tc::ex2;
 
 // act(z) and its derivative for two channels, from p = 1 / (1 + 2^(-z log2 e)). The product is rounded
 // before the exponential: an error of up to |z| 2^-24 in p, which bf16 data leave at that (2^-19 at

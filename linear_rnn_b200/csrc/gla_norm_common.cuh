@@ -27,19 +27,13 @@ namespace norm {
 
 using namespace sm100;
 using tc::f2;
+using tc::f2_add;
+using tc::f2_all;
 using tc::f2_fma;
 using tc::f2_mul;
+using tc::f2_split;
+using tc::f2_to_bf2;
 
-// ------------------------------------------------------------------ packed pairs of fp32
-__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ void f2_split(uint64_t v, float& lo, float& hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t f2_all(float v) { return f2(v, v); }
 __device__ __forceinline__ float f2_sum(uint64_t v) {
     float a, b;
     f2_split(v, a, b);
@@ -99,12 +93,6 @@ __device__ __forceinline__ void store_piece(float* p, const uint64_t (&v)[kPairs
             *reinterpret_cast<ulonglong2*>(p + 4 * i) = make_ulonglong2(v[2 * i], v[2 * i + 1]);
     }
 }
-__device__ __forceinline__ uint32_t to_bf16x2(uint64_t v) {
-    float a, b;
-    f2_split(v, a, b);
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
 template <int VEC>
 __device__ __forceinline__ void store_piece(__nv_bfloat16* p, const uint64_t (&v)[kPairs<VEC>]) {
     if constexpr (VEC == 1) {
@@ -112,12 +100,12 @@ __device__ __forceinline__ void store_piece(__nv_bfloat16* p, const uint64_t (&v
         f2_split(v[0], a, b);
         *p = __float2bfloat16_rn(a);
     } else if constexpr (VEC == 2) {
-        *reinterpret_cast<uint32_t*>(p) = to_bf16x2(v[0]);
+        *reinterpret_cast<uint32_t*>(p) = f2_to_bf2(v[0]);
     } else if constexpr (VEC == 8) {
         *reinterpret_cast<uint4*>(p) =
-            make_uint4(to_bf16x2(v[0]), to_bf16x2(v[1]), to_bf16x2(v[2]), to_bf16x2(v[3]));
+            make_uint4(f2_to_bf2(v[0]), f2_to_bf2(v[1]), f2_to_bf2(v[2]), f2_to_bf2(v[3]));
     } else {
-        *reinterpret_cast<uint2*>(p) = make_uint2(to_bf16x2(v[0]), to_bf16x2(v[1]));
+        *reinterpret_cast<uint2*>(p) = make_uint2(f2_to_bf2(v[0]), f2_to_bf2(v[1]));
     }
 }
 
@@ -138,7 +126,7 @@ __device__ __forceinline__ void store_pair(float* p, uint64_t v, bool half) {
     if (!half) p[1] = b;
 }
 __device__ __forceinline__ void store_pair(__nv_bfloat16* p, uint64_t v, bool half) {
-    const uint32_t w = to_bf16x2(v);
+    const uint32_t w = f2_to_bf2(v);
     if (!half && (reinterpret_cast<uintptr_t>(p) & 2) == 0) {
         *reinterpret_cast<uint32_t*>(p) = w;
         return;
@@ -160,8 +148,8 @@ __device__ __forceinline__ void put_piece(T* row, const Place& P, int j, const u
 constexpr int kRowElems = 16;
 __host__ __device__ constexpr int odd_room(int G) { return kRowElems * G + 16; }
 
-// S stages of shared memory that belong to the thread alone. Piece j of an input lies in units of up to 16 bytes,
-// blockDim units of that size apart from the next piece, so that a warp's accesses are contiguous.
+// S stages of shared memory that belong to the thread alone. Piece j of an input is a unit of 4, 8 or 16 bytes, blockDim
+// units of that size apart from the next piece, so that a warp's accesses are contiguous.
 // Stages are written by cp.async, one commit group per row; wait() leaves the groups of the S - 1 rows that
 // follow in flight.
 template <int S>
@@ -176,38 +164,25 @@ struct Feed {
 
     template <typename T, int VEC>
     __device__ __forceinline__ uint8_t* at(int stage, int thread_off, int j) const {
-        constexpr int B = VEC * (int)sizeof(T), U = B < 16 ? B : 16;
+        constexpr int B = VEC * (int)sizeof(T);
         uint8_t* d = mine + stage * stage_bytes + (thread_off + j * B) * (int)blockDim.x;
-        return U == 16 ? d : d - (16 - U) * (int)threadIdx.x;
+        return d - (16 - B) * (int)threadIdx.x;   // `mine` is 16 bytes a thread on
     }
     template <typename T, int VEC>
     __device__ __forceinline__ void copy(int stage, int thread_off, int j, const T* src) const {
         constexpr int B = VEC * (int)sizeof(T);
         uint8_t* d = at<T, VEC>(stage, thread_off, j);
-        if constexpr (B >= 16) {
-#pragma unroll
-            for (int u = 0; u < B / 16; ++u)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(d + u * 16 * (int)blockDim.x)),
-                             "l"(reinterpret_cast<const uint8_t*>(src) + 16 * u)
-                             : "memory");
+        if constexpr (B == 16) {
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(d)), "l"(src) : "memory");
         } else {
             static_assert(B == 4 || B == 8, "");
             asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(d)), "l"(src), "n"(B) : "memory");
         }
     }
     template <typename T, int VEC>
-    __device__ __forceinline__ void read(int thread_off, int j, uint64_t (&v)[kPairs<VEC>], size_t e0,
-                                         const Place& P) const {
-        constexpr int B = VEC * (int)sizeof(T);
-        const uint8_t* d = at<T, VEC>(s, thread_off, j);
-        if constexpr (B == 32) {   // eight fp32: two units
-            uint64_t a[2], b[2];
-            load_piece<4>(reinterpret_cast<const float*>(d), a);
-            load_piece<4>(reinterpret_cast<const float*>(d + 16 * (int)blockDim.x), b);
-            v[0] = a[0]; v[1] = a[1]; v[2] = b[0]; v[3] = b[1];
-        } else {
-            load_piece<VEC>(reinterpret_cast<const T*>(d), v);
-        }
+    __device__ __forceinline__ void read(int thread_off, int j, uint64_t (&v)[kPairs<VEC>], size_t,
+                                         const Place&) const {   // the row's place matters to a RowFeed only
+        load_piece<VEC>(reinterpret_cast<const T*>(at<T, VEC>(s, thread_off, j)), v);
     }
     __device__ __forceinline__ void commit() const { asm volatile("cp.async.commit_group;" ::: "memory"); }
     __device__ __forceinline__ void wait() const {
@@ -567,14 +542,17 @@ template <int V, int N, int S, int M, bool O = false> struct Shape {
 // BF16, F32: every operand of the row has that type, so pieces of 8, and a ring of single elements, exist too.
 // Blocks of up to 256 threads (D <= 4096 with pieces of 4 or 8) have kernels of their own, which need not fit their
 // registers into a larger block's share. Without a ring only rows beyond 8192 elements (up to 1024 threads, which
-// with 16 elements each spill), odd fp32 rows beyond 6656, and rows too long for two stages.
+// with 16 elements each spill 500 bytes and more), odd fp32 rows beyond 6656, and fp32 rows too long for two stages. The
+// backwards with two stages and 512 threads spill 32 to 96 bytes.
 template <int V, int N, int S, bool O = false, typename F>
 cudaError_t by_block(const RowPlan& p, F&& f) {
     return p.threads <= 256 ? f(Shape<V, N, S, 256, O>{}) : f(Shape<V, N, S, 512, O>{});
 }
-template <int V, int N, typename F>
-cudaError_t by_block(const RowPlan& p, F&& f) {   // no ring
-    return p.threads <= 512 ? f(Shape<V, N, 0, 512>{}) : f(Shape<V, N, 0, 1024>{});
+template <int V, int N, bool F32, typename F>
+cudaError_t no_ring(const RowPlan& p, F&& f) {
+    if constexpr (F32)
+        if (p.threads <= 512) return f(Shape<V, N, 0, 512>{});
+    return f(Shape<V, N, 0, 1024>{});   // with bf16 in the row always more threads
 }
 template <bool BF16, bool F32, bool WIDE, typename F>
 cudaError_t by_shape(const RowPlan& p, int stages, F&& f) {
@@ -586,11 +564,11 @@ cudaError_t by_shape(const RowPlan& p, int stages, F&& f) {
     if (p.vec == 1) {
         if constexpr (F32)
             if (p.nv == 4) return by_block<1, 4, 3>(p, f);   // three stages of 512 threads fit twice
-        return by_block<1, 16>(p, f);
+        return no_ring<1, 16, F32>(p, f);
     }
     if (p.vec == 2) {
         if (p.nv == 4) return stages == 3 ? by_block<2, 4, 3>(p, f) : f(Shape<2, 4, 2, 512>{});
-        return stages == 3 ? f(Shape<2, 8, 3, 512>{}) : stages == 2 ? f(Shape<2, 8, 2, 512>{}) : by_block<2, 8>(p, f);
+        return stages == 3 ? f(Shape<2, 8, 3, 512>{}) : stages == 2 ? f(Shape<2, 8, 2, 512>{}) : no_ring<2, 8, F32>(p, f);
     }
     if constexpr (WIDE)
         if (p.vec * p.nv == 8) {
@@ -605,7 +583,7 @@ cudaError_t by_shape(const RowPlan& p, int stages, F&& f) {
                                  : f(Shape<8, 2, 0, 1024>{});
     return stages == 3   ? by_block<4, 4, 3>(p, f)
            : stages == 2 ? f(Shape<4, 4, 2, 512>{})
-                         : by_block<4, 4>(p, f);
+                         : no_ring<4, 4, F32>(p, f);
 }
 template <typename F>
 cudaError_t by_kind(int kind, F&& f) {

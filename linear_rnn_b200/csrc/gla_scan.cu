@@ -47,23 +47,14 @@ constexpr int kFwdStages = 3;    // tiles of the forward's ring
 enum { LOAD_TMA = 0, LOAD_4 = 4, LOAD_2 = 2, LOAD_1 = 1 };
 
 // ------------------------------------------------------------------ packed pairs of fp32
+using tc::ex2;
 using tc::f2;
+using tc::f2_add;
+using tc::f2_all;
 using tc::f2_fma;
 using tc::f2_mul;
-__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ void f2_split(uint64_t v, float& lo, float& hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t f2_all(float v) { return f2(v, v); }
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
+using tc::f2_split;
+using tc::f2_to_bf2;
 __device__ __forceinline__ float rsqrt_approx(float x) {
     float y;
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -73,7 +64,8 @@ __device__ __forceinline__ float rsqrt_approx(float x) {
 // a = e^g and t = 1 - e^g for two channels. For -0.30 <= g <= 0.05, where a gate's memory is long
 // and an error in a is multiplied by 1 / (1 - a), t = -g P(g) with P the degree-4 polynomial closest
 // to (e^g - 1) / g there with P(0) = 1 (least largest relative error, 2.2e-8), so t is within 2 and
-// a = 1 - t within 1.3 units of 2^-24; elsewhere the hardware exponential serves (2^-22).
+// a = 1 - t within 1.3 units of 2^-24; elsewhere the hardware exponential serves (2^-22, and |g| 2^-24 from the rounding
+// of its argument).
 __device__ __forceinline__ void gate2(uint64_t g, uint64_t& a, uint64_t& t) {
     uint64_t s = f2_fma(g, f2_all(-0.007552224211394787f), f2_all(-0.041534192860126495f));
     s = f2_fma(g, s, f2_all(-0.1666625589132309f));
@@ -134,14 +126,8 @@ __device__ __forceinline__ void ld4(const __nv_bfloat16* p, uint64_t (&v)[2]) {
 __device__ __forceinline__ void st4(float* p, const uint64_t (&v)[2]) {
     *reinterpret_cast<ulonglong2*>(p) = make_ulonglong2(v[0], v[1]);
 }
-__device__ __forceinline__ uint32_t to_bf16x2(uint64_t v) {
-    float lo, hi;
-    f2_split(v, lo, hi);
-    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&b);
-}
 __device__ __forceinline__ void st4(__nv_bfloat16* p, const uint64_t (&v)[2]) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(to_bf16x2(v[0]), to_bf16x2(v[1]));
+    *reinterpret_cast<uint2*>(p) = make_uint2(f2_to_bf2(v[0]), f2_to_bf2(v[1]));
 }
 // Stores the channels c .. c+3 that exist, in pieces of PIECE (D is a multiple of it; p too is aligned to it).
 template <int PIECE>
@@ -170,7 +156,7 @@ __device__ __forceinline__ void put4(__nv_bfloat16* p, const uint64_t (&v)[2], i
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             if (PIECE == 2) {
-                if (c + 2 * k < D) *reinterpret_cast<uint32_t*>(p + 2 * k) = to_bf16x2(v[k]);
+                if (c + 2 * k < D) *reinterpret_cast<uint32_t*>(p + 2 * k) = f2_to_bf2(v[k]);
             } else {
                 float lo, hi;
                 f2_split(v[k], lo, hi);

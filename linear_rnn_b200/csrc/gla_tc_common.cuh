@@ -59,6 +59,12 @@ __device__ __forceinline__ float rcp_approx(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// 2^x by the hardware (relative error about 2^-22, subnormal inputs and results flushed to zero).
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 // Packed pairs of fp32 in one 64-bit register, multiplied lane-wise by the sm_100 packed
 // fp32 instruction (IEEE round-to-nearest per lane, like two separate multiplies).
@@ -77,6 +83,15 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ void f2_split(uint64_t v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t f2_all(float v) { return f2(v, v); }
 // bf16 pair (element 0 in the low half) -> fp32 pair
 __device__ __forceinline__ uint64_t bf2_to_f2(uint32_t w) {
     return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
