@@ -14,8 +14,8 @@
 // recurrence of the backward composes the same way from the other end with the same A.
 //
 // Bound by HBM (8 bytes an element forward, 14 backward in bf16) while enough CTAs are resident.
-// Measured, device time and share of the copy rate: forward 8 x 16 heads x 2048 x 64 27 us (0.77),
-// 8 heads x 65536 x 128 96 us (0.85); training pair 4 x 16 x 4096 x 256 284 us (0.79 of both calls' bytes).
+// Measured, device time and share of the copy rate: forward 8 x 16 heads x 2048 x 64 27.5 us (0.75),
+// 8 heads x 65536 x 128 102 us (0.80); training pair 4 x 16 x 4096 x 256 289 us (0.78 of both calls' bytes).
 #include <type_traits>
 
 #include "gla_common.cuh"
