@@ -512,15 +512,15 @@ inline int row_blocks(const RowPlan& p, long long rows, int heads) {
     if (most < 1) most = 1;
     return (int)(need < most ? need : most);
 }
-// Blocks of `kern` that an SM holds, asked of the runtime once per kernel, device, threads and group (`known`;
-// a kernel's shared memory follows from these; groups below a warp are 1, 2, 4, 8, 16).
-using Occupancy = std::atomic<int>[kMaxDevices][33 + 32];
+// Blocks of `kern` that an SM holds, asked of the runtime once per kernel, device and group (`known`; a kernel's threads
+// and shared memory follow from these: groups up to a warp stand in blocks of 256, longer ones are the block).
+using Occupancy = std::atomic<int>[kMaxDevices][33 + 33];
 template <typename K>
 int fit_blocks(K kern, const RowPlan& p, size_t smem, int blocks, int heads, Occupancy& known) {
     if ((long long)blocks * heads <= tc::num_sms()) return blocks;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return blocks;
-    std::atomic<int>& slot = known[dev][p.threads / 32 + (p.G < 32 ? 33 : 0) + (p.G < 32 ? p.G : 0)];
+    std::atomic<int>& slot = known[dev][p.G <= 32 ? 33 + p.G : p.G / 32];
     int per_sm = slot.load(std::memory_order_relaxed);
     if (per_sm == 0) {
         if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, p.threads, smem) != cudaSuccess ||
