@@ -343,8 +343,8 @@ GLA_API gla_status gla_mlstm_bwd_saved(const gla_problem* p, const void* q, cons
  *   as gla_scan_bwd).
  * ws: the backward's caller-owned device workspace of gla_scan_bwd_workspace_bytes(p) bytes (0 when p
  *   is invalid or unsupported), for the states; with `saved`, or without tokens, none is needed
- *   (NULL, 0; `saved` of 0 bytes may be NULL). The
- *   kernels' waits on their own copies are bounded, and one that gave up (a fault elsewhere on
+ *   (NULL, 0; `saved` of 0 bytes may be NULL).
+ * The kernels' waits on their own copies are bounded, and one that gave up (a fault elsewhere on
  *   the device) ends the call with results that are not valid rather than hanging, which
  *   gla_scan_check_device_status then reports.
  * Outputs may not overlap inputs, saved or ws. All pointers 16-byte aligned device memory.
