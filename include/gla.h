@@ -325,7 +325,7 @@ GLA_API gla_status gla_mlstm_bwd_saved(const gla_problem* p, const void* q, cons
  *   GLA_GATE_PER_KEY; chunk, scale and plan are ignored.
  * x, o, dO, dx [B,H,L,D] in io dtype; g, dg [B,H,L,D] f32; h0, hT, dhT, dh0 [B,H,D] f32.
  * g may be any real whose alpha is an fp32 number, g <= 88 (GLA_SCAN_NORM: g <= 0, where m is real; g = 0
- *   there, and |g| < 2^-126, gives m = 0, whose infinite slope is taken as 0). g = -inf is allowed:
+ *   there, and |g| < 2^-127, gives m = 0, whose infinite slope is taken as 0). g = -inf is allowed:
  *   alpha = 0, so that token starts anew (a packed document's first token); so does alpha < 2^-126.
  *   Products of alphas that leave fp32's range over many tokens do no harm where the states stay
  *   inside it; what they leave of a state below 2^-126 of its size may count as forgotten, whatever
