@@ -64,8 +64,8 @@ __device__ __forceinline__ float rsqrt_approx(float x) {
 // a = e^g and t = 1 - e^g for two channels. For -0.30 <= g <= 0.05, where a gate's memory is long
 // and an error in a is multiplied by 1 / (1 - a), t = -g P(g) with P the degree-4 polynomial closest
 // to (e^g - 1) / g there with P(0) = 1 (least largest relative error, 2.2e-8), so t is within 2 and
-// a = 1 - t within 1.3 units of 2^-24; elsewhere the hardware exponential serves (2^-22, and |g| 2^-24 from the rounding
-// of its argument).
+// a = 1 - t within 1.3 units of 2^-24; elsewhere the hardware exponential serves (2^-22, and |g| 2^-24 from
+// the rounding of its argument).
 __device__ __forceinline__ void gate2(uint64_t g, uint64_t& a, uint64_t& t) {
     uint64_t s = f2_fma(g, f2_all(-0.007552224211394787f), f2_all(-0.041534192860126495f));
     s = f2_fma(g, s, f2_all(-0.1666625589132309f));
@@ -255,8 +255,9 @@ struct ScanArgs {
 // strong gates it is 0, and an infinite state would become NaN. Both show: a state that is not finite stays so to the
 // end of a walk. So a walk composes, its end is looked at, and only where that is not finite the tile goes
 // again, with the steps that composition cannot take made token by token from the inputs in global memory (the
-// ring's stage may be free already). The look costs a long walk over clusters 2 % (8 heads x 65536 x 128: 104 us
-// without it, 106 with).
+// ring's stage may be free already). The look costs 1 to 3 %: forward 8 heads x 65536 x 128 102.6 -> 104.6 us, pair
+// 4 x 16 x 4096 x 256 292 -> 296. Rows that go again take up to 4 times as long, by tokens (an infinite state under
+// strong gates) 60 times.
 __device__ __forceinline__ bool is_finite(float v) { return fabsf(v) <= 3.402823466e38f; }
 // In any lane: the warp goes again as one, which spares the branch its bookkeeping.
 __device__ __forceinline__ bool any_not_finite(float v) { return __any_sync(0xffffffffu, !is_finite(v)); }
@@ -275,19 +276,26 @@ struct Tokens {
             if (A > 0.f && h == 0.f) return B;
         }
 #pragma unroll 1
-        for (int j = 0; j < n; ++j) {
-            const int t = t0 + (REV ? n - 1 - j : j);
-            if (t >= L) continue;
-            uint64_t a, u, inv;
-            gate2(f2(g[(size_t)t * D], 0.f), a, u);
-            const float w = to_f(v[(size_t)t * D]);
-            float a0, b0, none;
-            f2_split(a, a0, none);
-            if (REV) {
-                h = a0 * (w + h);
-            } else {
-                f2_split(times_factor2<IN>(in_factor2<IN>(u, inv), f2(w, 0.f)), b0, none);
-                h = fmaf(a0, h, b0);
+        for (int j0 = 0; j0 < n && h == h; j0 += RUN) {   // a run's loads together; the identity past L
+            float gv[RUN], w[RUN];
+#pragma unroll
+            for (int j = 0; j < RUN; ++j) {
+                const int t = t0 + (REV ? n - 1 - j0 - j : j0 + j);
+                gv[j] = t < L ? g[(size_t)t * D] : 0.f;
+                w[j] = t < L ? to_f(v[(size_t)t * D]) : 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < RUN; ++j) {
+                uint64_t a, u, inv;
+                gate2(f2(gv[j], 0.f), a, u);
+                float a0, b0, none;
+                f2_split(a, a0, none);
+                if (REV) {
+                    h = a0 * (w[j] + h);
+                } else {
+                    f2_split(times_factor2<IN>(in_factor2<IN>(u, inv), f2(w[j], 0.f)), b0, none);
+                    h = fmaf(a0, h, b0);
+                }
             }
         }
         return h;
@@ -296,7 +304,7 @@ struct Tokens {
 
 // Walks N runs of a channel in a tile (A and B of run r lie at r * CH) from run r0, REV: back from r0 + N - 1, with
 // state h: put(r, h) gets the state entering run r and may write it over the run's B. Returns the state after the
-// runs; kept: the B's, for another walk. walk_by_step is that one; t0 is the tile's first token.
+// runs; kept: the B's, for another walk.
 template <bool REV, int N, typename Put>
 __device__ __forceinline__ float walk_runs(const float* A, const float* B, int r0, float h, float (&kept)[N], Put put) {
 #pragma unroll
@@ -308,21 +316,6 @@ __device__ __forceinline__ float walk_runs(const float* A, const float* B, int r
     }
     return h;
 }
-template <bool REV, int N, typename Tok, typename Put>
-__device__ __forceinline__ float walk_by_step(const float* A, float* B, int r0, float h, const float (&kept)[N],
-                                              const Tok& tok, int t0, Put put) {
-#pragma unroll
-    for (int j = 0; j < N; ++j) B[(REV ? r0 + N - 1 - j : r0 + j) * CH] = kept[j];
-#pragma unroll 1
-    for (int j = 0; j < N; ++j) {
-        const int r = REV ? r0 + N - 1 - j : r0 + j;
-        const float ra = A[r * CH], rb = B[r * CH];
-        put(r, h);
-        h = tok.step(ra, rb, h, t0 + r * RUN, RUN);
-    }
-    return h;
-}
-
 // Sends (A, B) to every CTA of the cluster, waits for theirs and composes them onto `super` in
 // sequence order (reverse order for REV). Returns the value entering this CTA's tile; `super`
 // becomes the value leaving the row of tiles. Slots are used in turn, two rows of tiles apart: a
@@ -345,19 +338,35 @@ __device__ __forceinline__ float exchange(Tail& sm, int c, float A, float B, int
     }
     return in;
 }
-// The same row once more by Tokens::step; t0: the row's first token.
-template <bool REV, typename Tail, typename Tok>
-__device__ __forceinline__ float compose_by_step(const Tail& sm, int c, int cs, int rank, int i, float& super,
-                                                 const Tok& tok, int t0) {
-    float in = super;
+// Puts back what a walk over N runs from r0 replaced.
+template <int N>
+__device__ __forceinline__ void restore(float* B, int r0, const float (&kept)[N], bool rev) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) B[(rev ? r0 + N - 1 - j : r0 + j) * CH] = kept[j];
+}
+// The same once more by Tokens::step: the tiles of the row from its first token on (cs > 1; `super` becomes the value
+// leaving the row; else the value leaving the runs), then the N runs from r0 of this CTA's tile. row: the row's first
+// token. One loop for both, as code beside the fast path costs it time: with a copy of the step for each the long
+// forward takes 108 us instead of 104.5.
+template <bool REV, int N, typename Tok, typename Put>
+__device__ __forceinline__ void go_again(const float* A, const float* B, const float2* slot, int cs, int rank, int row,
+                                         int r0, float& super, const Tok& tok, Put put) {
+    float e = super, in = e;
+    int k = cs > 1 ? -cs : 0;
 #pragma unroll 1
-    for (int k = 0; k < cs; ++k) {
-        const int r = REV ? cs - 1 - k : k;
-        if (r == rank) in = super;
-        const float2 v = sm.slot[((i & 1) * cs + r) * CH + c];
-        super = tok.step(v.x, v.y, super, t0 + r * TT, TT);
+    for (; k < N; ++k) {
+        const bool tile = k < 0;
+        if (k == 0 && cs > 1) {
+            super = e;
+            e = in;
+        }
+        const int r = tile ? (REV ? -1 - k : cs + k) : (REV ? r0 + N - 1 - k : r0 + k);
+        if (tile && r == rank) in = e;
+        const float a = tile ? slot[r * CH].x : A[r * CH], b = tile ? slot[r * CH].y : B[r * CH];
+        if (!tile) put(r, e);
+        e = tok.step(a, b, e, tile ? row + r * TT : row + rank * TT + r * RUN, tile ? TT : RUN);
     }
-    return in;
+    if (cs == 1) super = e;
 }
 
 // Shared memory of the forward behind its ring: the runs' (A, B) of a tile, their start values, the
@@ -535,10 +544,9 @@ __global__ void __launch_bounds__(NT_F, 2)
             float h = walk_runs<false>(&sm.A[0][lane], &sm.B[0][lane], 0, in, kept, put);
             if (cs == 1) super = h;
             if (any_not_finite(super)) {
-                super = in = before;
-                if (cs > 1) in = compose_by_step<false>(sm, lane, cs, rank, i, super, tok, i * cs * TT);
-                h = walk_by_step<false>(&sm.A[0][lane], &sm.B[0][lane], 0, in, kept, tok, t0, put);
-                if (cs == 1) super = h;
+                super = before;
+                go_again<false, RUNS>(&sm.A[0][lane], &sm.B[0][lane], &sm.slot[(i & 1) * cs * CH + lane], cs, rank,
+                                      i * cs * TT, 0, super, tok, put);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.starts);
@@ -733,6 +741,7 @@ __global__ void __launch_bounds__(NT_F, 2)
         const bool live = c0 + lane < D;
         const size_t ns = cdiv(L, kSaveEvery);
         constexpr int NS = TT / kSaveEvery;   // saved states of a tile
+        static_assert(NS == 2, "");
         const size_t at = bh * L * D + c0 + lane;
         const Tokens<true, IN, T> back{P.g + at, static_cast<const T*>(P.dO) + at, D, L};
         const Tokens<false, IN, T> tok{P.g + at, static_cast<const T*>(P.x) + at, D, L};
@@ -764,20 +773,29 @@ __global__ void __launch_bounds__(NT_F, 2)
                 float d = walk_runs<true>(&sm.A[0][lane], &sm.R[0][lane], 0, in, kept, put);
                 if (cs == 1) super = d;
                 if (any_not_finite(super)) {
-                    super = in = before;
-                    if (cs > 1) in = compose_by_step<true>(sm, lane, cs, rank, i, super, back, t0 - rank * TT);
-                    d = walk_by_step<true>(&sm.A[0][lane], &sm.R[0][lane], 0, in, kept, back, t0, put);
-                    if (cs == 1) super = d;
+                    super = before;
+                    restore(&sm.R[0][lane], 0, kept, true);
+                    go_again<true, RUNS>(&sm.A[0][lane], &sm.R[0][lane], &sm.slot[(i & 1) * cs * CH + lane], cs, rank,
+                                         t0 - rank * TT, 0, super, back, put);
                 }
             }
+            constexpr int N = RUNS / NS;
+            auto put = [&](int r, float v) { sm.B[r][lane] = v; };
+            float kept[NS][N];
+            bool finite = true;
 #pragma unroll
             for (int n = 0; n < NS; ++n) {
-                constexpr int N = RUNS / NS;
-                auto put = [&](int r, float v) { sm.B[r][lane] = v; };
-                float kept[N];
-                float h = walk_runs<false>(&sm.A[0][lane], &sm.B[0][lane], n * N, sv[n], kept, put);
-                if (any_not_finite(h))
-                    walk_by_step<false>(&sm.A[0][lane], &sm.B[0][lane], n * N, sv[n], kept, tok, t0, put);
+                float h = walk_runs<false>(&sm.A[0][lane], &sm.B[0][lane], n * N, sv[n], kept[n], put);
+                finite = finite && is_finite(h);
+            }
+            if (__any_sync(0xffffffffu, !finite)) {
+#pragma unroll
+                for (int n = 0; n < NS; ++n) restore(&sm.B[0][lane], n * N, kept[n], false);
+#pragma unroll 1
+                for (int n = 0; n < NS; ++n) {
+                    float h = n ? sv[NS - 1] : sv[0];   // NS is 2
+                    go_again<false, N>(&sm.A[0][lane], &sm.B[0][lane], nullptr, 1, 0, t0, n * N, h, tok, put);
+                }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.starts);
